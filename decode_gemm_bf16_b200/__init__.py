@@ -11,9 +11,10 @@ The method: "CloudflareæŽ¨å‡ºUnweightç„¡æå£“ç¸®ç³»çµ±ï¼Œå°‡LLMæ¨¡åž‹å¤§å°å£“ç
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -30,6 +31,7 @@ PIPELINES = {"full": 0, "exponent": 1, "transcode": 2, "direct_palette": 3, "fus
 UW_VARIANT_AUTO, UW_VARIANT_TENSOR, UW_VARIANT_GEMV = 0, 1, 2
 VARIANTS = {"auto": 0, "tensor": 1, "gemv": 2}
 UW_FORM_HUFFMAN, UW_FORM_PALETTE = 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
 SECTIONS = ["sm", "vbits", "vpre", "vexp", "vcol", "idx", "stream", "chunk_off", "seg_rel", "lut"]
 
 # every entry point of include/unweight.h
@@ -40,7 +42,9 @@ EXPORTS = ["uw_status_str", "uw_version", "uw_last_device_status", "uw_compress_
            "uw_transcode_palette", "uw_gemm_workspace", "uw_gemm", "uw_dense_gemm_workspace",
            "uw_dense_gemm", "uw_autotune", "uw_gemm_direct_palette_noalloc", "uw_plan_resolve",
            "uw_plan_load_json", "uw_gemm_swiglu_workspace", "uw_gemm_swiglu",
-           "uw_sequence_workspace", "uw_gemm_sequence"]
+           "uw_sequence_workspace", "uw_gemm_sequence", "uw_mx_bytes", "uw_mx_quantize", "uw_mx_dequantize",
+           "uw_mx_gemm_workspace", "uw_mx_gemm", "uw_route_workspace", "uw_route", "uw_gemm_grouped_workspace",
+           "uw_gemm_grouped", "uw_combine"]
 
 
 class UnweightError(RuntimeError):
@@ -76,6 +80,19 @@ class GemmOpts(ctypes.Structure):
                 ("out_f32", ctypes.c_int32), ("variant", ctypes.c_int32), ("split_k", ctypes.c_int32),
                 ("stages", ctypes.c_int32), ("projection", ctypes.c_int32),
                 ("plan", ctypes.POINTER(PlanEntry)), ("plan_entries", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class MxDesc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class GroupArgs(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("x_rows", ctypes.c_int64), ("rows", ctypes.c_void_p), ("slots", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("E", ctypes.c_int32), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("W", ctypes.c_void_p), ("up", ctypes.c_void_p), ("W_mx", ctypes.POINTER(MxDesc)),
+                ("up_mx", ctypes.POINTER(MxDesc)), ("Y", ctypes.c_void_p), ("out_f32", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -120,6 +137,16 @@ def lib():
             "uw_gemm_direct_palette_noalloc": ([P, I64, P, P, I32, P], I32),
             "uw_autotune": ([ctypes.POINTER(P), I32, I32, ctypes.POINTER(I64), I32, ctypes.POINTER(P),
                              ctypes.POINTER(P), P, SZ, I32, ctypes.POINTER(PlanEntry), ctypes.c_char_p, P], I32),
+            "uw_mx_bytes": ([I64, I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)], I32),
+            "uw_mx_quantize": ([P, I32, I64, I64, I64, P, P, P], I32),
+            "uw_mx_dequantize": ([ctypes.POINTER(MxDesc), P, I32, P], I32),
+            "uw_mx_gemm_workspace": ([I64, I64, I64, I32, ctypes.POINTER(SZ)], I32),
+            "uw_mx_gemm": ([P, ctypes.POINTER(MxDesc), I64, ctypes.POINTER(MxDesc), P, I32, P, SZ, P], I32),
+            "uw_route_workspace": ([I64, I32, I32, ctypes.POINTER(SZ)], I32),
+            "uw_route": ([P, I32, I64, I32, I32, I32, I32, ctypes.c_float, P, P, P, P, P, P, SZ, P], I32),
+            "uw_gemm_grouped_workspace": ([ctypes.POINTER(GroupArgs), ctypes.POINTER(SZ)], I32),
+            "uw_gemm_grouped": ([ctypes.POINTER(GroupArgs), P], I32),
+            "uw_combine": ([P, I32, I64, P, P, I64, I32, I64, P, I32, P], I32),
             "uw_plan_load_json": ([ctypes.c_char_p, ctypes.POINTER(PlanEntry), I32, ctypes.POINTER(I32)], I32),
         }
         for name, (args, res) in sig.items():
@@ -497,3 +524,288 @@ def uw_plan_load_json(path: str, cap: int = 4096) -> list:
     n = ctypes.c_int32()
     _check(lib().uw_plan_load_json(path.encode(), arr, cap, ctypes.byref(n)), "uw_plan_load_json")
     return [_entry_dict(arr[i]) for i in range(min(n.value, cap))]
+
+
+# ---------------------------------------------------------------- microscaled 4-bit form and experts
+# These calls check their tensors (device, type, shape, layout), run on the
+# device that holds them whatever the current device is, and allocate outputs
+# and workspaces from torch's caching allocator on the stream they use, so that
+# calls on several streams and captured graphs never share a workspace unless
+# the caller passes one.
+_EMPTY_CTX = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """(context, stream handle): `device` current, and `stream` (default: the
+    device's current stream) current on it so that allocations belong to it."""
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        ctx = _EMPTY_CTX if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return ctx, handle
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _need(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t
+
+
+_BF16, _FLOAT, _I32, _U8 = (torch.bfloat16,), (torch.bfloat16, torch.float32), (torch.int32,), (torch.uint8,)
+
+
+def _input(t, name: str, dtypes, device=None) -> torch.Tensor:
+    """An input matrix: any strides (copied to rows of consecutive values when
+    it is not laid out so)."""
+    t = _need(t, name, dtypes, device=device, contiguous=False)
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _output(out, shape, out_f32: bool, device) -> torch.Tensor:
+    dtype = torch.float32 if out_f32 else torch.bfloat16
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _need(out, "out", (dtype,), shape, device)
+
+
+def _scratch(ws, nbytes: int, device) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _need(ws, "ws", _U8, device=device)
+
+
+class MxMatrix:
+    """A matrix [rows, K] (or a batch of them) in the microscaled 4-bit form:
+    packed codes uint8[..., rows, K/2] and the scale tiles uint8[batch * bytes]
+    (the layout is in the header; any shape of that many bytes)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        _need(codes, "codes", _U8)
+        if codes.dim() not in (2, 3):
+            raise ValueError(f"codes: expected [rows, K/2] or [batch, rows, K/2], got {tuple(codes.shape)}")
+        _need(scales, "scales", _U8, device=codes.device)
+        self.codes, self.scales = codes, scales
+        self.batch = codes.shape[0] if codes.dim() == 3 else 1
+        self.rows, self.K = codes.shape[-2], 2 * codes.shape[-1]
+        nb = uw_mx_bytes(self.batch, self.rows, self.K)[1]
+        if scales.numel() != nb:
+            raise ValueError(f"scales: expected {nb} bytes, got {scales.numel()}")
+        self._desc = MxDesc(codes.data_ptr(), scales.data_ptr(), self.batch, self.rows, self.K)
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def uw_mx_bytes(batch: int, rows: int, K: int) -> tuple:
+    """(code bytes, scale bytes) of `batch` matrices [rows, K]."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().uw_mx_bytes(int(batch), int(rows), int(K), ctypes.byref(c), ctypes.byref(s)), "uw_mx_bytes")
+    return c.value, s.value
+
+
+def uw_mx_quantize(X: torch.Tensor, out: Optional[MxMatrix] = None, stream=None) -> MxMatrix:
+    """X[rows, K] or [batch, rows, K] (BF16 or float32) to the microscaled 4-bit form."""
+    if isinstance(X, torch.Tensor) and X.dim() not in (2, 3):
+        raise ValueError(f"X: expected [rows, K] or [batch, rows, K], got {tuple(X.shape)}")
+    device = _need(X, "X", _FLOAT, contiguous=False).device
+    ctx, handle = _on(device, stream)
+    with ctx:
+        X = _input(X, "X", _FLOAT)
+        batch = X.shape[0] if X.dim() == 3 else 1
+        rows, K = X.shape[-2:]
+        if out is None:
+            nb = uw_mx_bytes(batch, rows, K)[1]
+            out = MxMatrix(torch.empty(*X.shape[:-1], K // 2, dtype=torch.uint8, device=device),
+                           torch.empty(nb, dtype=torch.uint8, device=device))
+        elif out.shape != tuple(X.shape) or out.device != device:
+            raise ValueError(f"out: expected {tuple(X.shape)} on {device}, got {out.shape} on {out.device}")
+        _check(lib().uw_mx_quantize(X.data_ptr(), 1 if X.dtype == torch.float32 else 0, batch, rows, K, out.codes.data_ptr(),
+                                    out.scales.data_ptr(), handle), "uw_mx_quantize")
+    return out
+
+
+def uw_mx_dequantize(m: MxMatrix, out: Optional[torch.Tensor] = None, out_f32: bool = False, stream=None) -> torch.Tensor:
+    """The values of a microscaled matrix, exactly."""
+    ctx, handle = _on(m.device, stream)
+    with ctx:
+        out = _output(out, m.shape, out_f32, m.device)
+        _check(lib().uw_mx_dequantize(ctypes.byref(m._desc), out.data_ptr(), 1 if out_f32 else 0, handle), "uw_mx_dequantize")
+    return out
+
+
+def uw_mx_gemm_workspace(M: int, N: int, K: int, x_mx: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().uw_mx_gemm_workspace(int(M), int(N), int(K), 1 if x_mx else 0, ctypes.byref(n)), "uw_mx_gemm_workspace")
+    return n.value
+
+
+def uw_mx_gemm(X, W: MxMatrix, out: Optional[torch.Tensor] = None, out_f32: bool = False, ws: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """Y[M, N] = X . W^T with W in the microscaled 4-bit form.  X: BF16 [M, K]
+    (the weights are rebuilt to BF16 on chip) or an MxMatrix (4-bit products)."""
+    device = W.device
+    mx = isinstance(X, MxMatrix)
+    if mx and X.device != device:
+        raise ValueError(f"X: on {X.device}, expected {device}")
+    ctx, handle = _on(device, stream)
+    with ctx:
+        if not mx:
+            X = _input(X, "X", _BF16, device)
+        if len(X.shape) != 2 or X.shape[1] != W.K:
+            raise ValueError(f"X: expected [M, {W.K}], got {tuple(X.shape)}")
+        M = X.shape[0]
+        need = uw_mx_gemm_workspace(M, W.rows, W.K, mx)
+        out = _output(out, (M, W.rows), out_f32, device)
+        ws = _scratch(ws, need, device)
+        _check(lib().uw_mx_gemm(None if mx else X.data_ptr(), ctypes.byref(X._desc) if mx else None, M, ctypes.byref(W._desc),
+                                out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel(), handle), "uw_mx_gemm")
+    return out
+
+
+class Route(NamedTuple):
+    """A router's choices (see uw_route in the header)."""
+    ids: torch.Tensor       # int32 [T, k]
+    weights: torch.Tensor   # float32 [T, k]
+    offsets: torch.Tensor   # int32 [E + 1]
+    rows: torch.Tensor      # int32 [T * k]
+    pos: torch.Tensor       # int32 [T, k]
+
+
+def uw_route_workspace(T: int, E: int, k: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().uw_route_workspace(int(T), int(E), int(k), ctypes.byref(n)), "uw_route_workspace")
+    return n.value
+
+
+def uw_route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = False, scale: float = 1.0,
+             ws: Optional[torch.Tensor] = None, stream=None) -> Route:
+    """The k experts of every token of logits[T, E] (BF16 or float32), their
+    weights, and the slots sorted by expert."""
+    if score not in SCORES:
+        raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
+    device = _need(logits, "logits", _FLOAT, contiguous=False).device
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [T, E], got {tuple(logits.shape)}")
+    ctx, handle = _on(device, stream)
+    with ctx:
+        logits = logits.contiguous()
+        T, E = logits.shape
+        need = uw_route_workspace(T, E, k)
+        i32 = dict(dtype=torch.int32, device=device)
+        r = Route(torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device=device), torch.empty(E + 1, **i32),
+                  torch.empty(T * k, **i32), torch.empty(T, k, **i32))
+        ws = _scratch(ws, need, device)
+        _check(lib().uw_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, T, E, int(k), SCORES[score],
+                              1 if renorm else 0, float(scale), r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
+                              r.rows.data_ptr(), r.pos.data_ptr(), ws.data_ptr(), ws.numel(), handle), "uw_route")
+    return r
+
+
+def _group_args(slots: int, E: int, N: int, K: int, W, up) -> GroupArgs:
+    a = GroupArgs()
+    a.slots, a.E, a.N, a.K = slots, E, N, K
+    if isinstance(W, MxMatrix):
+        a.W_mx = ctypes.pointer(W._desc)
+        if up is not None:
+            a.up_mx = ctypes.pointer(up._desc)
+    else:
+        a.W = W.data_ptr()
+        a.up = up.data_ptr() if up is not None else None
+    return a
+
+
+def _expert_weight(W, name: str):
+    """(E, N, K) of an expert weight."""
+    if isinstance(W, MxMatrix):
+        return W.batch, W.rows, W.K
+    _need(W, name, _BF16)
+    if W.dim() != 3:
+        raise ValueError(f"{name}: expected [E, N, K], got {tuple(W.shape)}")
+    return tuple(W.shape)
+
+
+def uw_gemm_grouped_workspace(slots: int, W, up=None) -> int:
+    E, N, K = _expert_weight(W, "W")
+    n = ctypes.c_size_t()
+    _check(lib().uw_gemm_grouped_workspace(ctypes.byref(_group_args(slots, E, N, K, W, up)), ctypes.byref(n)),
+           "uw_gemm_grouped_workspace")
+    return n.value
+
+
+def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, up=None,
+                    out: Optional[torch.Tensor] = None, out_f32: bool = False, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Y[s] = X[row(s)] . W[e]^T for the slots s of every expert e, that is
+    offsets[e] <= s < offsets[e + 1]; with `up`, silu(X . W^T) * (X . up^T).
+    W, up: BF16 [E, N, K] or MxMatrix with a batch of E.  rows: the row of X of
+    each slot (default: slot s reads row s).  Rows of the output outside the
+    offsets are left as they were."""
+    E, N, K = _expert_weight(W, "W")
+    device = W.device
+    if up is not None:
+        if isinstance(up, MxMatrix) != isinstance(W, MxMatrix):
+            raise ValueError("W and up: expected weights of one kind")
+        if _expert_weight(up, "up") != (E, N, K) or up.device != device:
+            raise ValueError(f"up: expected {(E, N, K)} on {device}")
+    _need(offsets, "offsets", _I32, (E + 1,), device)
+    if rows is not None:
+        _need(rows, "rows", _I32, device=device)
+        if rows.dim() != 1:
+            raise ValueError(f"rows: expected [slots], got {tuple(rows.shape)}")
+    ctx, handle = _on(device, stream)
+    with ctx:
+        X = _input(X, "X", _BF16, device)
+        if X.dim() != 2 or X.shape[1] != K:
+            raise ValueError(f"X: expected [rows, {K}], got {tuple(X.shape)}")
+        slots = X.shape[0] if rows is None else rows.shape[0]
+        a = _group_args(slots, E, N, K, W, up)
+        n = ctypes.c_size_t()
+        _check(lib().uw_gemm_grouped_workspace(ctypes.byref(a), ctypes.byref(n)), "uw_gemm_grouped_workspace")
+        out = _output(out, (slots, N), out_f32, device)
+        ws = _scratch(ws, n.value, device)
+        a.X, a.x_rows, a.offsets = X.data_ptr(), X.shape[0], offsets.data_ptr()
+        a.rows = rows.data_ptr() if rows is not None else None
+        a.Y, a.out_f32, a.workspace, a.workspace_bytes = out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel()
+        _check(lib().uw_gemm_grouped(ctypes.byref(a), handle), "uw_gemm_grouped")
+    return out
+
+
+def uw_combine(Z: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, out: Optional[torch.Tensor] = None,
+               out_f32: bool = False, stream=None) -> torch.Tensor:
+    """Y[t] = sum_j weights[t, j] * Z[pos[t, j]] over the choices with pos >= 0."""
+    device = _need(Z, "Z", _FLOAT, contiguous=False).device
+    if Z.dim() != 2:
+        raise ValueError(f"Z: expected [slots, N], got {tuple(Z.shape)}")
+    _need(pos, "pos", _I32, device=device)
+    if pos.dim() != 2:
+        raise ValueError(f"pos: expected [T, k], got {tuple(pos.shape)}")
+    _need(weights, "weights", (torch.float32,), pos.shape, device)
+    ctx, handle = _on(device, stream)
+    with ctx:
+        Z = _input(Z, "Z", _FLOAT)
+        T, k = pos.shape
+        out = _output(out, (T, Z.shape[1]), out_f32, device)
+        _check(lib().uw_combine(Z.data_ptr(), 1 if Z.dtype == torch.float32 else 0, Z.shape[0], pos.data_ptr(),
+                                weights.data_ptr(), T, k, Z.shape[1], out.data_ptr(), 1 if out_f32 else 0, handle), "uw_combine")
+    return out

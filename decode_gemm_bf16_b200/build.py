@@ -9,7 +9,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libunweight.so")
-SOURCES = ["uw_host.cpp", "uw_compress.cu", "uw_decode.cu", "uw_gemm.cu", "uw_gemv.cu"]
+SOURCES = ["uw_host.cpp", "uw_compress.cu", "uw_decode.cu", "uw_gemm.cu", "uw_gemv.cu", "uw_mx.cu",
+           "uw_route.cu", "uw_group.cu", "uw_experts.cpp"]
 HEADERS = ["uw_internal.h", "uw_device.cuh", os.path.join("..", "..", "include", "unweight.h")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 BUILD_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler",
@@ -71,7 +72,8 @@ def code_hash(unit: str | None = None) -> str:
 
 
 # translation unit of each measured kernel family
-KERNEL_UNITS = {"k_decode": "uw_decode.cu", "k_gemm": "uw_gemm.cu", "k_gemv": "uw_gemv.cu"}
+KERNEL_UNITS = {"k_decode": "uw_decode.cu", "k_gemm": "uw_gemm.cu", "k_gemv": "uw_gemv.cu",
+                "k_mx": "uw_mx.cu", "k_route": "uw_route.cu", "k_combine": "uw_route.cu", "k_group": "uw_group.cu"}
 
 
 def kernel_code_hash(kernel: str) -> str:

@@ -932,11 +932,30 @@ __global__ void __maxnreg__(80)
 }
 
 // ---------------------------------------------------------------- host side
+int pick_mg(int64_t M) {
+    int64_t mg = (M + 15) / 16 * 16;
+    if (mg > 256) mg = 256;
+    if (mg < 16) mg = 16;
+    return (int)mg;
+}
+
+// 48-bit call tags: a per-process random base plus a running count.
+unsigned long long next_epoch() {
+    static std::atomic<unsigned long long> ctr{0};
+    static const unsigned long long base = [] {
+        std::random_device rd;
+        return ((unsigned long long)rd() << 20) ^ (unsigned long long)rd();
+    }();
+    return (base + ctr.fetch_add(1)) & 0xFFFFFFFFFFFFull;
+}
+
+}  // namespace
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn() {
+static EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     if (!fn) {
         void* ptr = nullptr;
@@ -963,13 +982,6 @@ bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const voi
     return r == CUDA_SUCCESS;
 }
 
-int pick_mg(int64_t M) {
-    int64_t mg = (M + 15) / 16 * 16;
-    if (mg > 256) mg = 256;
-    if (mg < 16) mg = 16;
-    return (int)mg;
-}
-
 // cudaFuncSetAttribute once per (kernel, device, size): it is not free.
 cudaError_t set_smem_attr(const void* fn, int bytes) {
     static std::mutex mu;
@@ -985,16 +997,6 @@ cudaError_t set_smem_attr(const void* fn, int bytes) {
     return e;
 }
 
-// 48-bit call tags: a per-process random base plus a running count.
-unsigned long long next_epoch() {
-    static std::atomic<unsigned long long> ctr{0};
-    static const unsigned long long base = [] {
-        std::random_device rd;
-        return ((unsigned long long)rd() << 20) ^ (unsigned long long)rd();
-    }();
-    return (base + ctr.fetch_add(1)) & 0xFFFFFFFFFFFFull;
-}
-
 uint64_t timeout_ns() {
     static uint64_t t = 0;
     if (!t) {
@@ -1005,8 +1007,6 @@ uint64_t timeout_ns() {
     }
     return t;
 }
-
-}  // namespace
 
 int gemm_default_grid() { return num_sms(); }
 

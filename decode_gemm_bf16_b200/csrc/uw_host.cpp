@@ -185,16 +185,16 @@ extern "C" const char* uw_status_str(int s) {
     }
 }
 
-extern "C" int uw_version(void) { return 10100; }
+extern "C" int uw_version(void) { return 10200; }
 
 extern "C" uw_status uw_last_device_status(void* stream) {
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return UW_ERR_CUDA;
     }
-    int d = decode_status_take(), g = gemm_status_take();
-    if (d < 0 || g < 0) return UW_ERR_CUDA;
-    return (uw_status)(d ? d : g);
+    int d = decode_status_take(), g = gemm_status_take(), e = group_status_take(), r = route_status_take();
+    if (d < 0 || g < 0 || e < 0 || r < 0) return UW_ERR_CUDA;
+    return (uw_status)(d ? d : g ? g : e ? e : r);
 }
 
 static bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }

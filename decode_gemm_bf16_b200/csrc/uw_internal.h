@@ -79,6 +79,14 @@ int num_sms();
 // ---- device status words (one per kernel translation unit)
 int decode_status_take();
 int gemm_status_take();
+int group_status_take();
+int route_status_take();
+
+// ---- launch helpers (uw_gemm.cu)
+bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const void* base, uint64_t inner, uint64_t outer,
+                 uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+cudaError_t set_smem_attr(const void* fn, int bytes);
+uint64_t timeout_ns();   // bound of every device-side wait
 
 // ---- compress kernels (uw_compress.cu)
 struct CompressScratch {
@@ -193,5 +201,51 @@ constexpr int kGemvMaxM = 1;   // batches the GEMV kernel supports
 cudaError_t launch_gemv(const GemmArgs& a, cudaStream_t s, uw_status* st);
 int gemm_default_grid();
 unsigned long long gemm_next_epoch();
+
+// ---- microscaled form (uw_mx.cu)
+constexpr int kMxBlock = 32;        // values per scale
+constexpr int kMxTileRows = 128;    // a scale tile: 128 rows x 256 k, 1024 bytes
+constexpr int kMxTileK = 256;
+constexpr int kMxTileBytes = 1024;
+__host__ __device__ constexpr int64_t mx_row_tiles(int64_t rows) { return (rows + kMxTileRows - 1) / kMxTileRows; }
+__host__ __device__ constexpr int64_t mx_k_tiles(int64_t K) { return (K + kMxTileK - 1) / kMxTileK; }
+cudaError_t launch_mx_quantize(const void* X, int in_f32, int64_t batch, int64_t rows, int64_t K, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows, int64_t K,
+                                 void* out, int out_f32, cudaStream_t s);
+
+// ---- router and combination (uw_route.cu)
+constexpr int kRouteMaxE = 1024;
+constexpr int kRouteMaxK = 32;
+int route_blocks(int64_t T, int k);
+cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k, int score, int renorm, float scale,
+                         int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist,
+                         cudaStream_t s);
+cudaError_t launch_combine(const void* Z, int in_f32, int64_t slots, const int32_t* pos, const float* weights, int64_t T,
+                           int k, int64_t N, void* Y, int out_f32, cudaStream_t s);
+
+// ---- products of ragged groups (uw_group.cu)
+enum GroupSource { kGroupBf16 = 0, kGroupMx = 1, kGroupMxMx = 2 };
+struct GroupGemm {
+    int src = kGroupBf16;
+    const void* X = nullptr;             // BF16 [x_rows, K], or codes (kGroupMxMx)
+    const uint8_t* x_scales = nullptr;   // kGroupMxMx
+    int64_t x_rows = 0;
+    const int32_t* rows = nullptr;
+    int64_t slots = 0;
+    const int32_t* offsets = nullptr;    // NULL: one group [0, slots)
+    int E = 1;
+    int64_t N = 0, K = 0;
+    const void* W = nullptr;             // BF16, or codes
+    const void* up = nullptr;
+    const uint8_t* w_scales = nullptr;
+    const uint8_t* up_scales = nullptr;
+    void* Y = nullptr;
+    int out_f32 = 0;
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+};
+size_t group_ws_bytes(int src, int64_t slots, int E);
+cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st);
 
 }  // namespace uw

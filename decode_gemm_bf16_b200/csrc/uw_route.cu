@@ -1,0 +1,449 @@
+// uw_route.cu -- the ends of an expert layer: the router's choice with the
+// slots sorted by expert, and the weighted sum of the experts' outputs.
+//
+// Router.  The choice compares logits only (softmax and sigmoid rise with
+// the logit), by an order-preserving 32-bit key, so it is exact whatever the
+// scores round to.  A warp owns a token: E/32 keys a lane, k rounds of one
+// warp-wide maximum and one minimum over the indices that reach it.  Scores
+// are fp32 with the accurate exponential.
+// Slots.  A stable counting sort over at most one CTA per SM: CTA b owns a
+// contiguous run of tokens, counts its choices per expert (k_route_choose),
+// and after all counts are known (k_route_place) adds up the counts of the
+// CTAs before it, the experts before each expert and, inside the CTA, of the
+// warps before each warp.  Ranks inside a warp come from match_any, so the
+// order -- and every output -- is the same on every run.  What bounds it: the
+// logits are read once; below a few thousand tokens the launches' latency.
+// With few choices one CTA does both parts in a single launch.
+//
+// Combination.  Y[t] = sum_j w[t,j] Z[pos[t,j]]: bound by reading T k N and
+// writing T N values once; a thread owns 8 columns of one token and has its
+// first eight choices' rows in flight before it adds.
+#include "uw_device.cuh"
+#include "uw_internal.h"
+
+namespace uw {
+
+int route_status_take() { return unit_status_take(); }
+
+namespace {
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+struct RouteParams {
+    const void* logits;
+    int64_t T;
+    int E, k, score, renorm;
+    float scale;
+    int64_t chunk;   // tokens of a CTA
+    int32_t* ids;
+    float* weights;
+    int32_t* offsets;
+    int32_t* rows;
+    int32_t* pos;
+    int32_t* hist;   // [CTAs][E]
+};
+
+// Order-preserving key of a logit; 0: never chosen (NaN, -infinity).
+__device__ __forceinline__ uint32_t logit_key(float x) {
+    x = fminf(x, 3.402823466e38f) + 0.0f;   // +inf -> largest finite, -0 -> 0 (a NaN becomes the largest finite: see the caller)
+    const uint32_t b = __float_as_uint(x);
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+
+// One token: lane j < k ends up with choice j (expert id, or -1) and weight.
+template <int VPL, bool F32>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& id, float& w) {
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+        const int e = 32 * i + lane;
+        key[i] = 0;
+        if (e < p.E) {
+            const float x = F32 ? reinterpret_cast<const float*>(p.logits)[t * p.E + e]
+                                : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.logits)[t * p.E + e] << 16);
+            if (x == x && x != -INFINITY) key[i] = logit_key(x);
+        }
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; i++) best = best > key[i] ? best : key[i];
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    // softmax over every logit: the denominator, before keys are taken out
+    float total = 0.0f;
+    const float m = key_logit(top);   // top = 0 (no choice at all): unused
+    if (p.score == UW_SCORE_SOFTMAX && !p.renorm && top) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++)
+            if (key[i]) total += expf(key_logit(key[i]) - m);
+        total = warp_sum(total);
+    }
+    id = -1;
+    uint32_t mine = 0;
+    for (int j = 0; j < p.k; j++) {
+        const uint32_t mx = __reduce_max_sync(kFull, best);
+        if (mx == 0) break;
+        uint32_t cand = 0xFFFFFFFFu;
+        if (best == mx) {
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; i--)
+                if (key[i] == mx) cand = (uint32_t)(32 * i + lane);
+        }
+        const uint32_t e = __reduce_min_sync(kFull, cand);
+        if (cand == e) {   // this lane held it
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                if ((uint32_t)(32 * i + lane) == e) key[i] = 0;
+                best = best > key[i] ? best : key[i];
+            }
+        }
+        if (lane == j) {
+            id = (int)e;
+            mine = mx;
+        }
+    }
+    const float x = key_logit(mine);
+    float s = 0.0f;
+    if (mine) s = p.score == UW_SCORE_SOFTMAX ? expf(x - m) : 1.0f / (1.0f + expf(-x));
+    if (p.renorm) total = warp_sum(s);
+    if (p.score == UW_SCORE_SOFTMAX || p.renorm) s = total > 0.0f ? s / total : 0.0f;
+    w = mine ? s * p.scale : 0.0f;
+}
+
+// Positions of the CTA's choices, the offsets (CTA 0) and the rows of the
+// slots.  `sm` holds base[E], total[E + 1] and wcount[warps][E].
+__device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.E;
+    int32_t* base = sm;
+    int32_t* total = sm + E;
+    int32_t* wcount = total + E + 1;
+    for (int i = tid; i < 2 * E + 1 + kRouteWarps * E; i += kRouteThreads) sm[i] = 0;
+    __syncthreads();
+    // counts of the CTAs before this one, and of all: the threads cover E
+    // experts times as many row groups as fit
+    {
+        const int groups = kRouteThreads / E > 1 ? kRouteThreads / E : 1;
+        for (int i = tid; i < groups * E; i += kRouteThreads) {
+            const int e = i % E, g = i / E;
+            int before = 0, all = 0;
+#pragma unroll 8
+            for (int b = g; b < ctas; b += groups) {
+                const int c = __ldcg(p.hist + (int64_t)b * E + e);
+                all += c;
+                before += b < (int)blockIdx.x ? c : 0;
+            }
+            if (before) atomicAdd(&base[e], before);
+            if (all) atomicAdd(&total[e], all);
+        }
+    }
+    // this CTA's choices per warp: warp w owns a contiguous run of its entries
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
+    const int64_t first = t0 * p.k;
+    const int64_t n = t1 > t0 ? (t1 - t0) * p.k : 0;
+    const int64_t per = ((n + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
+    const int64_t w0 = first + (per * warp < n ? per * warp : n), w1 = first + (per * (warp + 1) < n ? per * (warp + 1) : n);
+    int32_t* mine = wcount + warp * E;
+    for (int64_t i = w0 + lane; i < w1; i += 32) {
+        const int e = p.ids[i];
+        if (e >= 0) atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    // exclusive prefix of the totals over the experts (warp 0, E/32 each)
+    if (warp == 0) {
+        const int each = (E + 31) / 32, lo = lane * each < E ? lane * each : E, hi = lo + each < E ? lo + each : E;
+        int sum = 0;
+        for (int e = lo; e < hi; e++) sum += total[e];
+        int run = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(kFull, run, d);
+            if (lane >= d) run += v;
+        }
+        int at = run - sum;
+        for (int e = lo; e < hi; e++) {
+            const int c = total[e];
+            total[e] = at;
+            at += c;
+        }
+        if (lane == 31) total[E] = run;
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kRouteThreads) {
+        int at = total[e] + base[e];
+        for (int w = 0; w < kRouteWarps; w++) {
+            const int c = wcount[w * E + e];
+            wcount[w * E + e] = at;
+            at += c;
+        }
+    }
+    if (blockIdx.x == 0)
+        for (int e = tid; e <= E; e += kRouteThreads) p.offsets[e] = total[e];
+    __syncthreads();
+    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int e = i < w1 ? p.ids[i] : -1;
+        const uint32_t same = __match_any_sync(kFull, e);
+        int slot = -1;
+        if (e >= 0) slot = mine[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == 31 - __clz(same)) mine[e] = slot + 1;
+        __syncwarp();
+        if (i < w1) {
+            p.pos[i] = slot;
+            if (slot >= 0) p.rows[slot] = (int32_t)(i / p.k);
+        }
+    }
+    // slots that no choice fills
+    const int64_t all = p.T * p.k;
+    for (int64_t i = total[E] + (int64_t)blockIdx.x * kRouteThreads + tid; i < all; i += (int64_t)ctas * kRouteThreads)
+        p.rows[i] = -1;
+}
+
+template <int VPL, bool F32>
+__global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParams p) {
+    extern __shared__ int32_t sm[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) sm[e] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
+    for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
+        int id;
+        float w;
+        choose<VPL, F32>(p, t, lane, id, w);
+        if (lane < p.k) {
+            p.ids[t * p.k + lane] = id;
+            p.weights[t * p.k + lane] = w;
+            if (id >= 0) atomicAdd(&sm[id], 1);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = sm[e];
+    if (gridDim.x == 1) {   // a single CTA places its choices at once
+        __threadfence();
+        __syncthreads();
+        place(p, sm, 1);
+    }
+}
+
+__global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams p) {
+    extern __shared__ int32_t sm[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    place(p, sm, (int)gridDim.x);
+}
+
+template <typename P>
+cudaError_t launch_pdl(void (*kern)(const P), int64_t grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+typedef void (*RouteKernel)(const RouteParams);
+template <bool F32>
+RouteKernel route_kernel(int E) {
+    return E <= 32    ? k_route_choose<1, F32>
+           : E <= 64  ? k_route_choose<2, F32>
+           : E <= 128 ? k_route_choose<4, F32>
+           : E <= 256 ? k_route_choose<8, F32>
+           : E <= 512 ? k_route_choose<16, F32>
+                      : k_route_choose<32, F32>;
+}
+
+// ---------------------------------------------------------------- combination
+constexpr int kCombineThreads = 256;
+constexpr int kCombineCols = 8;     // columns of a thread
+constexpr int kCombineAhead = 8;    // rows in flight
+
+struct CombineParams {
+    const void* Z;
+    int64_t slots;
+    const int32_t* pos;
+    const float* weights;
+    int64_t T;
+    int k;
+    int64_t N;
+    int64_t groups;   // column groups of 8
+    void* Y;
+};
+
+template <bool F32>
+__device__ __forceinline__ void load_cols(const void* Z, int64_t at, int n, bool vec, float (&v)[8]) {
+    if (vec) {
+        if (F32) {
+            const float4* z = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(Z) + at);
+            const float4 a = __ldg(z), b = __ldg(z + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(Z) + at));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            v[i] = 0.0f;
+            if (i < n)
+                v[i] = F32 ? reinterpret_cast<const float*>(Z)[at + i]
+                           : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(Z)[at + i] << 16);
+        }
+    }
+}
+
+// Rows of N values are 16-byte aligned runs of 8 columns when N % 8 == 0;
+// otherwise every value is loaded and stored by itself.
+template <bool IN32, bool OUT32>
+__global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
+    if (i >= p.T * p.groups) return;
+    const int64_t t = i / p.groups, c = (i - t * p.groups) * kCombineCols;
+    const bool vec = p.N % 8 == 0;
+    const int n = p.N - c < 8 ? (int)(p.N - c) : 8;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kCombineAhead) {
+        float z[kCombineAhead][8], w[kCombineAhead];
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; j++) {
+            w[j] = 0.0f;
+            int32_t s = -1;
+            if (j0 + j < p.k) {
+                s = __ldg(p.pos + t * p.k + j0 + j);
+                w[j] = __ldg(p.weights + t * p.k + j0 + j);
+            }
+            if (s >= p.slots) {
+                raise_status(UW_ERR_DEVICE);
+                s = -1;
+            }
+            if (s >= 0) {
+                load_cols<IN32>(p.Z, s * p.N + c, n, vec, z[j]);
+            } else {
+                w[j] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; q++) z[j][q] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; j++)
+#pragma unroll
+            for (int q = 0; q < 8; q++) acc[q] = fmaf(w[j], z[j][q], acc[q]);
+    }
+    const int64_t at = t * p.N + c;
+    if (OUT32) {
+        float* y = reinterpret_cast<float*>(p.Y) + at;
+        if (vec) {
+            __stcs(reinterpret_cast<float4*>(y), make_float4(acc[0], acc[1], acc[2], acc[3]));
+            __stcs(reinterpret_cast<float4*>(y) + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                if (q < n) y[q] = acc[q];
+        }
+    } else {
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.Y) + at;
+        if (vec) {
+            uint4 o;
+            uint32_t* op = &o.x;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * q], acc[2 * q + 1]);
+                op[q] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            __stcs(reinterpret_cast<uint4*>(y), o);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                if (q < n) y[q] = __float2bfloat16_rn(acc[q]);
+        }
+    }
+}
+
+}  // namespace
+
+// CTAs of the router: one up to 512 choices (a single launch), else up to one
+// per SM, 8 tokens at least in each.
+int route_blocks(int64_t T, int k) {
+    if (T * k <= 512) return 1;
+    const int64_t b = (T + 7) / 8;
+    return (int)(b < num_sms() ? b : num_sms());
+}
+
+cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k, int score, int renorm, float scale,
+                         int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist,
+                         cudaStream_t s) {
+    RouteParams p{};
+    p.logits = logits;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.score = score;
+    p.renorm = renorm;
+    p.scale = scale;
+    const int ctas = route_blocks(T, k);
+    p.chunk = (T + ctas - 1) / ctas;
+    p.ids = ids;
+    p.weights = weights;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.pos = pos;
+    p.hist = hist;
+    const size_t smem = (size_t)(2 * E + 1 + kRouteWarps * E) * 4;
+    const RouteKernel choose_k = in_f32 ? route_kernel<true>(E) : route_kernel<false>(E);
+    const size_t smem_c = ctas == 1 ? smem : (size_t)E * 4;
+    cudaError_t e = smem_c > 48 * 1024 ? set_smem_attr((const void*)choose_k, (int)smem_c) : cudaSuccess;
+    if (e == cudaSuccess && smem > 48 * 1024) e = set_smem_attr((const void*)k_route_place, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(choose_k, ctas, kRouteThreads, smem_c, s, p);
+    if (e != cudaSuccess || ctas == 1) return e;
+    return launch_pdl<RouteParams>(k_route_place, ctas, kRouteThreads, smem, s, p);
+}
+
+cudaError_t launch_combine(const void* Z, int in_f32, int64_t slots, const int32_t* pos, const float* weights, int64_t T,
+                           int k, int64_t N, void* Y, int out_f32, cudaStream_t s) {
+    CombineParams p{};
+    p.Z = Z;
+    p.slots = slots;
+    p.pos = pos;
+    p.weights = weights;
+    p.T = T;
+    p.k = k;
+    p.N = N;
+    p.groups = (N + kCombineCols - 1) / kCombineCols;
+    p.Y = Y;
+    const int64_t grid = (T * p.groups + kCombineThreads - 1) / kCombineThreads;
+    void (*kern)(const CombineParams) = in_f32 ? (out_f32 ? k_combine<true, true> : k_combine<true, false>)
+                                               : (out_f32 ? k_combine<false, true> : k_combine<false, false>);
+    return launch_pdl<CombineParams>(kern, grid, kCombineThreads, 0, s, p);
+}
+
+}  // namespace uw

@@ -367,6 +367,140 @@ uw_status uw_gemm_swiglu(const uint16_t* X, int64_t M, const uw_blob* gate, cons
 uw_status uw_gemm_direct_palette_noalloc(const uint16_t* X, int64_t M, const uw_blob* blob, void* Y,
                                          int out_f32, void* stream);
 
+/* ---------------------------------------------------------------- microscaled 4-bit form
+ * An addition of this library; the pages have no counterpart.  Where the
+ * lossless form is too large, weights (or activations) can be kept in the
+ * microscaling format MXFP4 (OCP Microscaling Formats 1.0): 32 consecutive
+ * values of a row share one power-of-two scale 2^s, and a value is a sign and
+ * one of the eight magnitudes {0, 0.5, 1, 1.5, 2, 3, 4, 6} (e2m1), so
+ * value = magnitude * 2^s.
+ *   Quantisation of a block of 32 with largest magnitude a:
+ *     s = clamp(floor(log2 a) - 2, -127, 127), -127 for a = 0; every value
+ *     divided by 2^s is rounded to the nearest magnitude, ties to the even
+ *     code, above 6 to 6, its sign kept (also that of a zero).  A block that
+ *     holds a NaN or an infinity gets the scale NaN and codes 0: all its
+ *     values read back as NaN.
+ *   codes: u8[batch][rows][K/2], value 2i of a row in the low nibble of byte
+ *     i: bit 3 the sign, bits 0..2 the magnitude's index.
+ *   scales: s + 127 as one byte (255: NaN), in tiles of 1024 bytes that cover
+ *     128 rows x 256 k, in the order a tensor core reads them.  With
+ *     KT = ceil(K/256), byte of row r, block b = k/32 of matrix i:
+ *       ((i * ceil(rows/128) + r/128) * KT + b/8) * 1024
+ *         + (b/4 % 2) * 512 + (r % 32) * 16 + (r/32 % 4) * 4 + b % 4
+ *     Bytes of rows and blocks past the matrix are 0 (uw_mx_quantize writes
+ *     them; whoever builds the plane by hand does the same).
+ * K is a positive multiple of 64, rows * K at most 2^31 - 256 per matrix, as
+ * everywhere.  Pointers are 16-byte aligned. */
+typedef struct {
+    const uint8_t* codes;    /* device, uw_mx_bytes' code_bytes                              */
+    const uint8_t* scales;   /* device, uw_mx_bytes' scale_bytes                             */
+    int64_t batch, rows, K;  /* `batch` matrices [rows, K]                                   */
+} uw_mx_matrix;
+
+uw_status uw_mx_bytes(int64_t batch, int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes);
+
+/* X: device [batch, rows, K], BF16 or (in_f32) float32, to codes and scales.
+ * rows = 0 or batch = 0 is a no-op. */
+uw_status uw_mx_quantize(const void* X, int in_f32, int64_t batch, int64_t rows, int64_t K, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+
+/* out: device [batch, rows, K], BF16 or (out_f32) float32: the values, exactly
+ * (a magnitude that passes the type's range, possible only with scales above
+ * 2^125, becomes an infinity). */
+uw_status uw_mx_dequantize(const uw_mx_matrix* m, void* out, int out_f32, void* stream);
+
+/* Y[M,N] = X[M,K] . W^T with W one MXFP4 matrix [N, K] (batch 1), accumulated
+ * in float32 on the tensor cores and rounded once.  Exactly one of X, X_mx:
+ *   X: device BF16 [M,K]; the weights are rebuilt to BF16 on chip, which is
+ *     exact wherever BF16 holds the value.
+ *   X_mx: MXFP4 [M,K] (batch 1; M = its rows): block-scaled 4-bit products.
+ * Y: device [M,N], BF16 or float32 (out_f32), 16-byte aligned.  M = 0 is a
+ * no-op.  workspace: 256-byte aligned, any contents, owned by the call until
+ * it completes (a captured call owns it whenever its graph runs). */
+uw_status uw_mx_gemm_workspace(int64_t M, int64_t N, int64_t K, int x_mx, size_t* bytes);
+
+uw_status uw_mx_gemm(const uint16_t* X, const uw_mx_matrix* X_mx, int64_t M, const uw_mx_matrix* W, void* Y, int out_f32,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- experts
+ * An addition of this library; the pages have no counterpart.  The MLP of a
+ * mixture of experts: a router chooses k of E experts for each of T tokens
+ * (uw_route), the experts' gate, up and down projections are products of
+ * ragged groups of rows (uw_gemm_grouped), and each token's outputs are added
+ * with the router's weights (uw_combine).  A slot is one (token, choice) pair;
+ * slots are sorted by (expert, token, choice).  All sizes stay on the device:
+ * no call waits for the host to read the groups.  Serving only, like the rest
+ * of the library: no gradients. */
+
+/* logits: device [T, E], BF16 or (in_f32) float32.  A logit of NaN counts as
+ * -infinity, +infinity as the largest finite number, -0 as 0.  Every token
+ * takes its k largest logits, ties by the lower index; an expert with logit
+ * -infinity is never taken, so a token may have fewer than k choices, and a
+ * padded token whose logits are all -infinity has none.
+ *   ids[T, k]: the experts by falling logit; -1: no choice.
+ *   weights[T, k]: UW_SCORE_SOFTMAX: softmax over all E logits (renorm: over
+ *     the chosen); UW_SCORE_SIGMOID: sigmoid of each logit (renorm: divided by
+ *     the chosen ones' sum, 0 if that is 0); times `scale`; 0: no choice.
+ *   offsets[E + 1]: expert e owns slots offsets[e] .. offsets[e+1]-1.
+ *   rows[T * k]: the token of each slot, -1 from slot offsets[E] on.
+ *   pos[T, k]: the slot of each choice, -1: no choice.
+ * 1 <= k <= 32, k <= E <= 1024, T * k < 2^31.  T = 0 writes offsets only.
+ * workspace: 256-byte aligned, any contents. */
+enum { UW_SCORE_SOFTMAX = 0, UW_SCORE_SIGMOID = 1 };
+
+uw_status uw_route_workspace(int64_t T, int E, int k, size_t* bytes);
+
+uw_status uw_route(const void* logits, int in_f32, int64_t T, int E, int k, int score, int renorm, float scale,
+                   int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Y[s, n] = sum_k X[row(s), k] W[e(s), n, k] for every slot s of every expert;
+ * with `up` (or up_mx): Y = silu(X . W^T) * (X . up^T), both products in one
+ * pass over X.  Accumulated in float32, rounded once.
+ *   X: device BF16 [x_rows, K], 16-byte aligned.  rows: NULL (slot s reads row
+ *     s; x_rows >= slots) or the row of each slot, device int32[slots].
+ *   offsets: device int32[E + 1], not falling, at most `slots`; rows of Y at
+ *     or past offsets[E] (and before offsets[0]) are left as they were.
+ *     Offsets that fall or pass `slots`, or a row index outside [0, x_rows) in
+ *     a group, raise UW_ERR_DEVICE in the device status word; the rows
+ *     concerned are unspecified, no access leaves the buffers.
+ *   W / up: device BF16 [E, N, K], or W_mx / up_mx: MXFP4 (batch E, rows N).
+ *     Both of one kind.  E <= 1024, E * N <= 2^31 - 256.
+ *   Y: device [slots, N], BF16 or float32 (out_f32), 16-byte aligned.
+ *   workspace: 256-byte aligned, any contents, owned by the call until it
+ *     completes (a captured call owns it whenever its graph runs). */
+typedef struct {
+    const uint16_t* X;
+    int64_t x_rows;
+    const int32_t* rows;
+    int64_t slots;
+    const int32_t* offsets;
+    int32_t E;
+    int64_t N, K;
+    const uint16_t* W;
+    const uint16_t* up;
+    const uw_mx_matrix* W_mx;
+    const uw_mx_matrix* up_mx;
+    void* Y;
+    int32_t out_f32;
+    void* workspace;
+    size_t workspace_bytes;
+} uw_group_args;
+
+/* Reads slots, E, N, K and which weights are given; pointers may be NULL
+ * otherwise. */
+uw_status uw_gemm_grouped_workspace(const uw_group_args* args, size_t* bytes);
+
+uw_status uw_gemm_grouped(const uw_group_args* args, void* stream);
+
+/* Y[t, n] = sum_j weights[t, j] Z[pos[t, j], n] over the choices with
+ * pos >= 0, in float32 in the order of j, rounded once; a token without
+ * choices gets zeros.  Z: device [slots, N], BF16 or (in_f32) float32; Y:
+ * device [T, N], BF16 or float32 (out_f32); both 16-byte aligned.  A pos at or
+ * past `slots` raises UW_ERR_DEVICE and adds nothing.  1 <= k <= 32. */
+uw_status uw_combine(const void* Z, int in_f32, int64_t slots, const int32_t* pos, const float* weights, int64_t T, int k,
+                     int64_t N, void* Y, int out_f32, void* stream);
+
 /* ---------------------------------------------------------------- autotune
  * §自動調優機制: a measured coordinate descent.  For each batch size in Ms:
  * start every projection at the first feasible candidate, then sweep the
