@@ -745,11 +745,13 @@ def _expert_weight(W, name: str):
     return tuple(W.shape)
 
 
-def uw_gemm_grouped_workspace(slots: int, W, up=None) -> int:
+def uw_gemm_grouped_workspace(slots: int, W, up=None, gathered: bool = False) -> int:
+    """Workspace bytes of uw_gemm_grouped (gathered: with `rows`)."""
     E, N, K = _expert_weight(W, "W")
+    a = _group_args(slots, E, N, K, W, up)
+    a.rows = 4 if gathered else None   # read as given or not
     n = ctypes.c_size_t()
-    _check(lib().uw_gemm_grouped_workspace(ctypes.byref(_group_args(slots, E, N, K, W, up)), ctypes.byref(n)),
-           "uw_gemm_grouped_workspace")
+    _check(lib().uw_gemm_grouped_workspace(ctypes.byref(a), ctypes.byref(n)), "uw_gemm_grouped_workspace")
     return n.value
 
 
@@ -780,12 +782,12 @@ def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[to
             raise ValueError(f"X: expected [rows, {K}], got {tuple(X.shape)}")
         slots = X.shape[0] if rows is None else rows.shape[0]
         a = _group_args(slots, E, N, K, W, up)
+        a.rows = rows.data_ptr() if rows is not None else None
         n = ctypes.c_size_t()
         _check(lib().uw_gemm_grouped_workspace(ctypes.byref(a), ctypes.byref(n)), "uw_gemm_grouped_workspace")
         out = _output(out, (slots, N), out_f32, device)
         ws = _scratch(ws, n.value, device)
         a.X, a.x_rows, a.offsets = X.data_ptr(), X.shape[0], offsets.data_ptr()
-        a.rows = rows.data_ptr() if rows is not None else None
         a.Y, a.out_f32, a.workspace, a.workspace_bytes = out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel()
         _check(lib().uw_gemm_grouped(ctypes.byref(a), handle), "uw_gemm_grouped")
     return out

@@ -29,7 +29,7 @@ uw_status check_mx(const uw_mx_matrix* m) {
     uw_status st = check_matrices(m->batch, m->rows, m->K);
     if (st) return st;
     if (m->batch * m->rows == 0) return UW_OK;
-    if (!m->codes || !m->scales || !aligned(m->codes, 16) || !aligned(m->scales, 16)) return UW_ERR_INVALID_ARG;
+    if (!m->codes || !m->scales || !aligned(m->codes, 32) || !aligned(m->scales, 16)) return UW_ERR_INVALID_ARG;
     return UW_OK;
 }
 
@@ -56,6 +56,10 @@ uw_status check_group(const uw_group_args* a, int* src) {
     return check_weight(a->E, a->N, a->K);
 }
 
+size_t group_bytes(int src, const uw_group_args* a) {
+    return group_ws_bytes(src, a->slots, a->E, a->N, a->K, a->up || a->up_mx, a->rows != nullptr);
+}
+
 }  // namespace
 
 // ===========================================================================
@@ -75,7 +79,7 @@ extern "C" uw_status uw_mx_quantize(const void* X, int in_f32, int64_t batch, in
     uw_status st = check_matrices(batch, rows, K);
     if (st) return st;
     if (batch * rows == 0) return UW_OK;
-    if (!X || !codes || !scales || !aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return UW_ERR_INVALID_ARG;
+    if (!X || !codes || !scales || !aligned(X, 16) || !aligned(codes, 32) || !aligned(scales, 16)) return UW_ERR_INVALID_ARG;
     return cuda_ok(launch_mx_quantize(X, in_f32, batch, rows, K, codes, scales, (cudaStream_t)stream));
 }
 
@@ -92,7 +96,7 @@ extern "C" uw_status uw_mx_gemm_workspace(int64_t M, int64_t N, int64_t K, int x
     uw_status st = check_weight(1, N, K);
     if (st) return st;
     if (M > 0x7FFFFFFF - 256) return UW_ERR_SHAPE;
-    *bytes = group_ws_bytes(x_mx ? kGroupMxMx : kGroupMx, M, 1);
+    *bytes = group_ws_bytes(x_mx ? kGroupMxMx : kGroupMx, M, 1, N, K, false, false);
     return UW_OK;
 }
 
@@ -164,7 +168,7 @@ extern "C" uw_status uw_gemm_grouped_workspace(const uw_group_args* a, size_t* b
     int src;
     uw_status st = check_group(a, &src);
     if (st) return st;
-    *bytes = group_ws_bytes(src, a->slots, a->E);
+    *bytes = group_bytes(src, a);
     return UW_OK;
 }
 
@@ -188,7 +192,7 @@ extern "C" uw_status uw_gemm_grouped(const uw_group_args* a, void* stream) {
     if (!a->offsets || !aligned(a->offsets, 4) || !aligned(a->rows, 4)) return UW_ERR_INVALID_ARG;
     if (a->x_rows < 1 || (!a->rows && a->x_rows < a->slots)) return UW_ERR_INVALID_ARG;
     if (a->x_rows > 0x7FFFFFFF - 256) return UW_ERR_SHAPE;
-    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < group_ws_bytes(src, a->slots, a->E))
+    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < group_bytes(src, a))
         return UW_ERR_WORKSPACE;
     GroupGemm g;
     g.src = src;

@@ -20,14 +20,35 @@
 //     contiguous range a CTA, so every SM reads until the end.  The CTA with a
 //     cut tile's first k steps reaches it last and adds the others' fp32
 //     partial rows in k order (from the workspace; deterministic);
-//   * warp roles: 0-3 epilogue, 4 TMA producer, 5 MMA issue, and for 4-bit
-//     weights with BF16 rows 6-21 rebuild (codes -> BF16 in tensor memory, the
-//     MMA's A operand).  Rows are gathered by the TMA (four row indices a
-//     request);
-//   * MXFP4 with MXFP4 rows: block-scaled MMA, the scale bytes go from shared
-//     to tensor memory (tcgen05.cp) in the order the format stores them;
+//   * warp roles: 0-3 epilogue, 4 TMA producer, 5 MMA issue (6: see kMix; 6-21:
+//     see kGroupMx);
+//   * 4-bit weights with BF16 rows (kGroupMx8): the tensor cores take the codes
+//     and scales as they are, against 8-bit rows.  A BF16 value has 8
+//     significant bits, an e4m3 value 4: x = 2^s (hi + lo/16) with both in
+//     e4m3 and 2^s the scale of its block of 32 is exact for every x of at
+//     least 2^-13 times the block's largest, and off by at most 2^-21 of that
+//     largest below.  hi and lo are two rows of the MMA's N, added in fp32 at
+//     the end: the operations of a BF16 product at twice the rate, and no
+//     rebuilt weights.  A first kernel (k_group_split) writes the rows of
+//     every tile in the order of its stages' shared memory, gathered, split
+//     and swizzled, so a stage's rows and scales are one bulk copy;
+//   * K an odd multiple of 64 (kGroupMx): the TMA's unpacking load wants rows
+//     of 128 codes, so warps 6-21 rebuild codes to BF16 in tensor memory, the
+//     MMA's A operand;
+//   * MXFP4 with MXFP4 rows (kGroupMxMx): block-scaled 4-bit MMA; the scale
+//     bytes go from shared to tensor memory (tcgen05.cp) in the order the
+//     format stores them;
+//   * gathered BF16 rows: tiles of up to 32 slots take them by TMA (four row
+//     indices a request), larger ones from a gathered copy (k_group_gather):
+//     a request of four rows of 128 bytes takes about 34 cycles, a row of a
+//     box about 2;
+//   * after one of these two kernels the weights of the first stages are
+//     requested before the wait on it: it lets this kernel start only after
+//     its own wait, so everything it does not write is complete;
 //   * every wait is bounded; on expiry the CTA raises UW_ERR_TIMEOUT, drains
 //     its own copies and MMAs, frees tensor memory and returns.
+#include <cuda_fp16.h>
+
 #include "uw_device.cuh"
 #include "uw_internal.h"
 
@@ -40,6 +61,8 @@ namespace {
 constexpr int kTileN = 128;            // weight rows of a tile
 constexpr int kProd = 4, kMma = 5, kRebuild0 = 6, kRebuildWarps = 16;
 constexpr int kThreadsPlain = 6 * 32;
+constexpr int kMix = 6;                // kGroupMx8: warp that joins the scales of two weights
+constexpr int kThreadsMix = 7 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
 constexpr int kMaxS = 12;              // stages
 constexpr int kMaxT = 8;               // rebuilt-A slots in tensor memory
@@ -55,9 +78,15 @@ struct GroupParams {
     const int32_t* offsets;
     int E, kt, MG, box, n_tiles, up, out_f32, y_vec;
     int S, T, nacc;
+    uint32_t acc_w;                         // columns of an accumulator
     uint32_t stage_bytes, off_s, off_b;     // codes (or BF16 weights) at 0, scale bytes, X
     uint32_t sf_a_bytes, sf_b_bytes;        // scale bytes of a stage: weights (one matrix), X
+    uint32_t sf_slot;                       // scale columns of a stage
     uint32_t a_col0, sf_col0;
+    int early;                              // a preparing kernel of this call ran just before
+    const uint8_t* prep;                    // kGroupMx8: [slot tiles][kt][scales, rows]
+    int64_t prep_chunk;                     // bytes of one stage of one tile there
+    int part_f4;                            // float4 columns of a partial row
     uint32_t ctrl_off, stg_off, tab_off;
     const uint8_t* sw;                      // scale tiles of W, up, X
     const uint8_t* su;
@@ -100,6 +129,7 @@ struct Seg {
 struct Tile {
     int e, n, rows;          // expert, weight tile, slots of the tile
     int64_t s0;              // first slot
+    int64_t m;               // the slot tile's number among all
 };
 
 // Units of CTA b's range start here; owner of a unit.
@@ -154,6 +184,7 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int
     t.n = l / nb;
     const int m = band * kBand + l % nb;
     t.s0 = (int64_t)pl.begin[lo] + (int64_t)m * p.MG;
+    t.m = pl.cum[lo] / p.n_tiles + m;
     t.rows = c - m * p.MG < p.MG ? c - m * p.MG : p.MG;
     return t;
 }
@@ -246,28 +277,120 @@ __device__ __forceinline__ void rebuild32(const uint4 c, uint32_t s, uint32_t (&
     }
 }
 
-__device__ __forceinline__ uint32_t swizzled(int row_bytes, int r, int c) {
-    return row_bytes == 128  ? r * 128 + ((c ^ (r & 7)) << 4)
-           : row_bytes == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
-                             : r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+// 16-byte chunk c of row r in rows of 32 bytes stored with the 32-byte swizzle.
+__device__ __forceinline__ uint32_t sw32(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
+
+// D (+)= A * B^T, A e2m1 (a byte each), B e4m3, one e8m0 scale per 32 k (K = 32).
+__device__ __forceinline__ void tc_mma_mx8(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
 }
 
-// SRC: kGroupBf16 (KB = 64 k a stage), kGroupMx (64, 128 or 256), kGroupMxMx (256).
-template <int SRC, int KB>
+// Instruction descriptor of kind::mxf8f6f4: A e2m1, B e4m3, scales e8m0, both
+// K-major, M = 128; `id` (0..3) picks the scale byte.
+__device__ __forceinline__ uint32_t idesc_mx8(int N, uint32_t id) {
+    return (id << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+}
+
+// Columns of the MMA's N for a tile of `rows` slots: the rows rounded up to
+// 16; two of them (hi, lo) per row rounded up to 8 for split rows.
+template <int SRC>
+__device__ __forceinline__ int mma_n(int rows) {
+    return SRC == kGroupMx8 ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;
+}
+
+// The tile list from the offsets, by one warp: 32 runs of experts, one a lane.
+// Tables in shared memory: cum[E + 1], begin[E], count[E].
+__device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int64_t slots, int MG, int n_tiles, int32_t* cum,
+                                           int32_t* begin, int32_t* count, int lane) {
+    const int each = (E + 31) / 32, lo = lane * each < E ? lane * each : E, hi = lo + each < E ? lo + each : E;
+    int sum = 0;
+    bool bad = false;
+    for (int e = lo; e < hi; e++) {
+        int64_t b = 0, n = slots;
+        if (offsets) {
+            const int64_t o0 = offsets[e], o1 = offsets[e + 1];
+            bad |= o0 < 0 || o1 < o0 || o1 > slots;
+            b = o0 < 0 ? 0 : o0 > slots ? slots : o0;
+            n = (o1 > slots ? slots : o1) - b;
+            if (n < 0) n = 0;
+        }
+        begin[e] = (int)b;
+        count[e] = (int)n;
+        sum += (int)((n + MG - 1) / MG) * n_tiles;
+    }
+    int run = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (lane >= d) run += v;
+    }
+    int at = run - sum;
+    for (int e = lo; e < hi; e++) {
+        cum[e] = at;
+        at += (count[e] + MG - 1) / MG * n_tiles;
+    }
+    if (lane == 31) cum[E] = run;
+    if (__any_sync(0xFFFFFFFFu, bad)) {   // offsets that fall or pass the slots: no tiles at all
+        for (int e = lane; e <= E; e += 32) cum[e] = 0;
+        if (bad) raise_status(UW_ERR_DEVICE);
+    }
+}
+
+// k of a stage.
+constexpr int stage_k(int src) { return src == kGroupMx8 ? 128 : src == kGroupMxMx ? 256 : 64; }
+
+// Bytes that a stage of tile t receives.
+template <int SRC>
+__device__ __forceinline__ uint32_t stage_tx(const GroupParams& p, const Tile& t) {
+    const int nN = mma_n<SRC>(t.rows);
+    uint32_t x = (uint32_t)((nN + p.box - 1) / p.box * p.box) * 128u;
+    if (SRC == kGroupMx8) x = (uint32_t)nN * 128u;
+    else if (p.rows) x = (uint32_t)((t.rows + 3) / 4) * 512u;
+    // the unpacking load counts the packed bytes of its rows
+    return (uint32_t)kTileN * (SRC == kGroupMx ? 32u : SRC == kGroupMx8 ? 64u : 128u) + p.sf_a_bytes * (p.up ? 2u : 1u) + p.sf_b_bytes + x;
+}
+
+// Weight rows (64 of each matrix, or 128) and their scales of one stage.
+template <int SRC>
+__device__ __forceinline__ void load_weights(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
+                                             const Tile& t, int kt, uint32_t st, uint32_t fb) {
+    constexpr int KB = stage_k(SRC);
+    constexpr uint32_t kARow = SRC == kGroupMx ? 32 : 128;
+    const int n0 = t.n * (p.up ? kTileN / 2 : kTileN);
+    const int64_t wrow = (int64_t)t.e * p.N + n0;
+    const int ax = SRC == kGroupBf16 || SRC == kGroupMx8 ? kt * KB : kt * (KB / 2);   // codes unpacked by the TMA count as elements
+    tma_load_2d(st, &tm_w, ax, (int)wrow, fb);
+    tma_load_2d(st + kTileN / 2 * kARow, p.up ? &tm_u : &tm_w, ax, (int)(p.up ? wrow : wrow + kTileN / 2), fb);
+    if (SRC != kGroupBf16) {
+        // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
+        const int64_t at = ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes +
+                           (SRC == kGroupMxMx  ? (int64_t)kt * kMxTileBytes
+                            : SRC == kGroupMx8 ? (int64_t)kt * (kMxTileBytes / 2)
+                                               : (int64_t)(kt >> 1) * (kMxTileBytes / 2));
+        bulk_load(st + p.off_s, p.sw + at, p.sf_a_bytes, fb);
+        if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, p.su + at, p.sf_a_bytes, fb);
+    }
+}
+
+template <int SRC>
 __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
                                            const GroupParams& p) {
-    constexpr bool kMx = SRC != kGroupBf16;
+    constexpr int KB = stage_k(SRC);
     constexpr bool kRe = SRC == kGroupMx;
-    constexpr int kARow = SRC == kGroupBf16 ? 128 : KB / 2;          // bytes of a weight row in a stage
-    constexpr int kHalves = SRC == kGroupMxMx ? 1 : KB / 64;         // 128-byte slabs of X
-    constexpr int kGroups = KB == 64 ? 2 : 1;                        // rebuild groups (alternate stages)
+    constexpr bool kScaled = SRC == kGroupMx8 || SRC == kGroupMxMx;   // scales in tensor memory
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ctrl_off);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxS, recon = empty + 8 * kMaxS, tfree = recon + 8 * kMaxT;
-    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxS + 2 * kMaxT + 5);
+    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxS + 2 * kMaxT + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* cum = reinterpret_cast<int32_t*>(smem + p.tab_off);
     int32_t* begin = cum + p.E + 1;
@@ -278,9 +401,10 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         for (int s = 0; s < p.S; s++) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
+            mbar_init(mixed + 8 * s, 1);
         }
         for (int t = 0; t < p.T; t++) {
-            mbar_init(recon + 8 * t, kRebuildWarps / kGroups);
+            mbar_init(recon + 8 * t, kRebuildWarps / 2);
             mbar_init(tfree + 8 * t, 1);
         }
         for (int a = 0; a < 2; a++) {
@@ -300,44 +424,16 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_u);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // With a preparing kernel before this one the offsets and weights are
+    // complete already (see k_group_split); what it writes is waited for below.
+    if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 0) {
-        // the tile list: 32 runs of experts, one a lane
-        const int each = (p.E + 31) / 32, lo = lane * each < p.E ? lane * each : p.E, hi = lo + each < p.E ? lo + each : p.E;
-        int sum = 0;
-        bool bad = false;
-        for (int e = lo; e < hi; e++) {
-            int64_t b = 0, n = p.slots;
-            if (p.offsets) {
-                const int64_t o0 = p.offsets[e], o1 = p.offsets[e + 1];
-                bad |= o0 < 0 || o1 < o0 || o1 > p.slots;
-                b = o0 < 0 ? 0 : o0 > p.slots ? p.slots : o0;
-                n = (o1 > p.slots ? p.slots : o1) - b;
-                if (n < 0) n = 0;
-            }
-            begin[e] = (int)b;
-            count[e] = (int)n;
-            sum += (int)((n + p.MG - 1) / p.MG) * p.n_tiles;
-        }
-        int run = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, run, d);
-            if (lane >= d) run += v;
-        }
-        int at = run - sum;
-        for (int e = lo; e < hi; e++) {
-            cum[e] = at;
-            at += (count[e] + p.MG - 1) / p.MG * p.n_tiles;
-        }
-        if (lane == 31) cum[p.E] = run;
-        if (bad) raise_status(UW_ERR_DEVICE);
-    }
+    if (warp == 0) list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     Plan pl;
     pl.cum = cum;
@@ -357,77 +453,72 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     if (warp == kProd) {
         // ------------------------------------------------------------ TMA producer
         const bool leader = elect_one();
-        Walk wk(pl, blockIdx.x);
+        int64_t q = 0, pre = 0;
         Seg sg;
+        if (p.early) {
+            // the first stages' weights and scales, before the wait on the preparing kernel
+            Walk w0(pl, blockIdx.x);
+            while (pre < p.S && w0.next(pl, p.kt, sg)) {
+                const Tile t = locate(p, pl, sg.tile);
+                for (int kt = sg.kt0; kt < sg.kt1 && pre < p.S; kt++, pre++)
+                    if (leader) {
+                        mbar_arrive_expect_tx(full + 8 * (uint32_t)pre, stage_tx<SRC>(p, t));
+                        load_weights<SRC>(p, tm_w, tm_u, t, kt, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre);
+                    }
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
+        Walk wk(pl, blockIdx.x);
         Ring r;
-        int64_t q = 0;
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
             const Tile t = locate(p, pl, sg.tile);
-            const int nN = (t.rows + 15) & ~15;
-            const int n0 = t.n * rows_a;
-            const int64_t wrow = (int64_t)t.e * p.N + n0;
+            const int nN = mma_n<SRC>(t.rows);
             const int boxes = (nN + p.box - 1) / p.box;
-            const uint32_t x_bytes = p.rows ? (uint32_t)nN * 128u * kHalves : (uint32_t)(boxes * p.box) * 128u * kHalves;
-            const uint32_t tx = kTileN * kARow + x_bytes + (kMx ? p.sf_a_bytes * (p.up ? 2 : 1) : 0) +
-                                (SRC == kGroupMxMx ? p.sf_b_bytes : 0);
-            int4 idx[2] = {};
-            if (p.rows) {
-                // rows past the tile's end repeat its last one (their columns are never stored)
+            int4 idx = {};
+            if (p.rows && lane < (t.rows + 3) / 4) {
+                // four rows a lane; past the tile's end its last row again (never stored)
+                int* ip = &idx.x;
 #pragma unroll
-                for (int g = 0; g < 2; g++) {
-                    int* ip = &idx[g].x;
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int at = 4 * (lane + 32 * g) + i;
-                        const int32_t v = p.rows[t.s0 + (at < t.rows ? at : t.rows - 1)];
-                        const bool in = v >= 0 && v < p.x_rows;
-                        if (!in) raise_status(UW_ERR_DEVICE);
-                        ip[i] = in ? v : 0;
-                    }
+                for (int i = 0; i < 4; i++) {
+                    const int at = 4 * lane + i;
+                    const int32_t v = p.rows[t.s0 + (at < t.rows ? at : t.rows - 1)];
+                    const bool in = v >= 0 && v < p.x_rows;
+                    if (!in) raise_status(UW_ERR_DEVICE);
+                    ip[i] = in ? v : 0;
                 }
             }
-            const uint8_t* sfw = kMx ? p.sw + ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes : nullptr;
-            const uint8_t* sfu = kMx && p.up ? p.su + ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes : nullptr;
             for (int kt = sg.kt0; kt < sg.kt1; kt++, q++, r.advance(p.S)) {
-                if (!mbar_wait(empty + 8 * r.i, r.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
                 const uint32_t st = base + (uint32_t)r.i * p.stage_bytes, fb = full + 8 * r.i;
-                if (leader) {
-                    mbar_arrive_expect_tx(fb, tx);
-                    const int ax = SRC == kGroupBf16 ? kt * KB : kt * (KB / 2);
-                    tma_load_2d(st, &tm_w, ax, (int)wrow, fb);
-                    tma_load_2d(st + kTileN / 2 * kARow, p.up ? &tm_u : &tm_w, ax, (int)(p.up ? wrow : wrow + kTileN / 2), fb);
-                    if (kMx) {
-                        // the stage's part of a scale tile (256 k): all, one half, or the half that holds it
-                        const int64_t so = KB == 256 ? (int64_t)kt * kMxTileBytes
-                                                     : (int64_t)(KB == 128 ? kt : kt >> 1) * (kMxTileBytes / 2);
-                        bulk_load(st + p.off_s, sfw + so, p.sf_a_bytes, fb);
-                        if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, sfu + so, p.sf_a_bytes, fb);
+                if (q >= pre) {
+                    if (!mbar_wait(empty + 8 * r.i, r.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
+                    if (leader) {
+                        mbar_arrive_expect_tx(fb, stage_tx<SRC>(p, t));
+                        load_weights<SRC>(p, tm_w, tm_u, t, kt, st, fb);
                     }
+                }
+                if (SRC == kGroupMx8) {
+                    // scales and rows of the stage, one run in both memories
+                    if (leader)
+                        bulk_load(st + p.off_b - p.sf_b_bytes, p.prep + (t.m * p.kt + kt) * p.prep_chunk,
+                                  p.sf_b_bytes + (uint32_t)nN * 128u, fb);
+                } else if (p.rows) {
+                    __syncwarp();
+                    if (lane < (t.rows + 3) / 4) tma_gather4(st + p.off_b + (uint32_t)lane * 512u, &tm_x, kt * KB, idx, fb);
+                } else if (leader) {
                     if (SRC == kGroupMxMx) {
                         const int64_t rt = t.s0 / kMxTileRows;
                         for (uint32_t i = 0; i < p.sf_b_bytes / kMxTileBytes; i++) {
                             // a row tile past the last reads the last one again (rows past the end: never stored)
                             const int64_t last = (p.x_rows - 1) / kMxTileRows, at = rt + i < last ? rt + i : last;
-                            bulk_load(st + p.off_s + p.sf_a_bytes + i * kMxTileBytes, p.sx + (at * p.k_tiles + kt) * kMxTileBytes,
-                                      kMxTileBytes, fb);
+                            bulk_load(st + p.off_b - p.sf_b_bytes + i * kMxTileBytes,
+                                      p.sx + (at * p.k_tiles + kt) * kMxTileBytes, kMxTileBytes, fb);
                         }
                     }
-                    if (!p.rows)
-                        for (int h = 0; h < kHalves; h++)
-                            for (int b = 0; b < boxes; b++)
-                                tma_load_2d(st + p.off_b + (uint32_t)(h * p.MG + b * p.box) * 128u, &tm_x,
-                                            SRC == kGroupMxMx ? kt * (KB / 2) : kt * KB + 64 * h, (int)(t.s0 + b * p.box), fb);
+                    for (int b = 0; b < boxes; b++)
+                        tma_load_2d(st + p.off_b + (uint32_t)(b * p.box) * 128u, &tm_x, kt * (SRC == kGroupMxMx ? KB / 2 : KB),
+                                    (int)(t.s0 + b * p.box), fb);
                 }
-                __syncwarp();
-                if (p.rows)
-#pragma unroll
-                    for (int g = 0; g < 2; g++) {
-                        const int at = 4 * (lane + 32 * g);
-                        if (at < nN)
-                            for (int h = 0; h < kHalves; h++)
-                                tma_gather4(st + p.off_b + (uint32_t)(h * p.MG + at) * 128u, &tm_x, kt * KB + 64 * h, idx[g], fb);
-                    }
             }
         }
         if (!ok)   // every load already issued lands before the CTA exits
@@ -442,47 +533,52 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
             const Tile t = locate(p, pl, sg.tile);
-            const int nN = (t.rows + 15) & ~15;
+            const int nN = mma_n<SRC>(t.rows);
             const uint32_t idesc = mma_idesc_bf16(kTileN, nN);
             if (!mbar_wait(acce + 8 * ra.i, ra.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(ra.i * p.MG);
+            const uint32_t acc = tmem + (uint32_t)ra.i * p.acc_w;
             for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
                 if (kRe && !mbar_wait(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
+                if (SRC == kGroupMx8 && p.up && !mbar_wait(mixed + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (leader) {
                     const uint32_t st = base + (uint32_t)r.i * p.stage_bytes;
-                    if (SRC == kGroupMxMx) {
-                        // scales of the stage: weights 2 x 4 columns, then X 2 x (4 per 128 slots)
-                        const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
-                        const uint32_t sfa = tmem + p.sf_col0 + (uint32_t)r.i * (8u + 8u * nb), sfb = sfa + 8u;
-                        const uint32_t ss = st + p.off_s;
+                    const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + p.off_b);
+                    if (kScaled) {
+                        // scales of the stage, 4 columns per 512 bytes: weights, then rows
+                        const uint32_t sfa = tmem + p.sf_col0 + (uint32_t)r.i * p.sf_slot, ss = st + p.off_s;
+                        const uint32_t sfb = sfa + (SRC == kGroupMxMx ? 8u : 4u), sb = st + p.off_b - p.sf_b_bytes;
+                        if (SRC == kGroupMxMx) {
+                            const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
 #pragma unroll
-                        for (uint32_t h = 0; h < 2; h++) {
-                            tc_copy_scales(sfa + 4u * h, ss + 512u * h);
-                            for (uint32_t i = 0; i < nb; i++)
-                                tc_copy_scales(sfb + 4u * (h * nb + i), ss + p.sf_a_bytes + kMxTileBytes * i + 512u * h);
+                            for (uint32_t h = 0; h < 2; h++) {
+                                tc_copy_scales(sfa + 4u * h, ss + 512u * h);
+                                for (uint32_t i = 0; i < nb; i++)
+                                    tc_copy_scales(sfb + 4u * (h * nb + i), sb + kMxTileBytes * i + 512u * h);
+                            }
+#pragma unroll
+                            for (uint32_t j = 0; j < 4; j++)
+                                tc_mma_mx(acc, ad + 2u * j, bd + 2u * j, idesc_mx(nN, 2u * (j & 1u)), sfa + 4u * (j >> 1),
+                                          sfb + 4u * nb * (j >> 1), kt > sg.kt0 || j > 0 ? 1u : 0u);
+                        } else {
+                            tc_copy_scales(sfa, p.up ? ss + 1024u : ss);
+                            for (uint32_t i = 0; i < p.sf_b_bytes / 512u; i++) tc_copy_scales(sfb + 4u * i, sb + 512u * i);
+#pragma unroll
+                            for (uint32_t j = 0; j < 4; j++)
+                                tc_mma_mx8(acc, ad + 2u * j, bd + 2u * j, idesc_mx8(nN, j), sfa, sfb,
+                                           kt > sg.kt0 || j > 0 ? 1u : 0u);
                         }
-                        const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + p.off_b);
-#pragma unroll
-                        for (uint32_t j = 0; j < 4; j++)
-                            tc_mma_mx(acc, ad + 2u * j, bd + 2u * j, idesc_mx(nN, 2u * (j & 1u)), sfa + 4u * (j >> 1),
-                                      sfb + 4u * nb * (j >> 1), kt > sg.kt0 || j > 0 ? 1u : 0u);
                     } else {
-                        const uint64_t ad = sw128_desc(st);
                         const uint32_t ta = tmem + p.a_col0 + (uint32_t)(KB / 2) * (uint32_t)rt.i;
 #pragma unroll
-                        for (int h = 0; h < kHalves; h++) {
-                            const uint64_t bd = sw128_desc(st + p.off_b + (uint32_t)(h * p.MG) * 128u);
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                const uint32_t more = kt > sg.kt0 || h > 0 || j > 0 ? 1u : 0u;
-                                if (kRe)
-                                    tc_mma_tmem_a(acc, ta + 8u * (uint32_t)(4 * h + j), bd + 2u * j, idesc, more);
-                                else
-                                    tc_mma(acc, ad + 2u * j, bd + 2u * j, idesc, more);
-                            }
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t more = kt > sg.kt0 || j > 0 ? 1u : 0u;
+                            if (kRe)
+                                tc_mma_tmem_a(acc, ta + 8u * (uint32_t)j, bd + 2u * j, idesc, more);
+                            else
+                                tc_mma(acc, ad + 2u * j, bd + 2u * j, idesc, more);
                         }
                     }
                     tc_commit(empty + 8 * r.i);
@@ -498,16 +594,42 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         if (leader) tc_commit(fin);
         mbar_wait(fin, 0, p.timeout, nullptr);
         __syncwarp();
+    } else if (SRC == kGroupMx8 && warp == kMix) {
+        // ------------------------------------------------------------ scales of two weights
+        // The tile's 128 rows are 64 of W and 64 of `up`, halves of a 128-row
+        // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
+        // either into the 16 bytes that tensor memory takes for lane l.
+        if (p.up) {
+            Walk wk(pl, blockIdx.x);
+            Seg sg;
+            Ring r;
+            bool ok = true;
+            while (ok && wk.next(pl, p.kt, sg)) {
+                const Tile t = locate(p, pl, sg.tile);
+                for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
+                    if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
+                    const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
+                    const uint32_t at = ss + (uint32_t)(lane * 16 + (t.n & 1) * 8);
+                    const uint32_t to = ss + 1024u + (uint32_t)(lane * 16);
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; i++) {
+                        sts32(to + 4u * i, lds32(at + 4u * i));
+                        sts32(to + 8u + 4u * i, lds32(at + 512u + 4u * i));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(mixed + 8 * r.i);
+                }
+            }
+        }
     } else if (kRe && warp >= kRebuild0) {
         // ------------------------------------------------------------ rebuild
-        // Warp w owns tensor-memory lanes (weight rows) 32 (w % 4) ..; the four
-        // warps of a quarter (two with two groups) share the stage's pieces of
-        // 32 k.  S and T are even with two groups, so a group meets the same
-        // slots in every round and sees all their phases in turn.
-        constexpr int kPieces = KB / 32;
-        constexpr int kPer = kPieces * 4 * kGroups / kRebuildWarps;   // pieces of a warp
-        const int rw = warp - kRebuild0, grp = kGroups == 2 ? rw / 8 : 0;
-        const int quarter = warp & 3, sub = (kGroups == 2 ? rw % 8 : rw) >> 2;
+        // Warp w owns tensor-memory lanes (weight rows) 32 (w % 4) ..; two groups
+        // of eight take alternate stages, two warps of a quarter one piece of
+        // 32 k each.  S and T are even, so a group meets the same slots in
+        // every round and sees all their phases in turn.
+        const int rw = warp - kRebuild0, grp = rw / 8;
+        const int quarter = warp & 3, pc = (rw % 8) >> 2;
         const int row = 32 * quarter + lane;
         Walk wk(pl, blockIdx.x);
         Seg sg;
@@ -524,23 +646,17 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             }
             so += (uint32_t)(lane * 16 + sq * 4);
             for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S), rt.advance(p.T)) {
-                if (kGroups == 2 && (rt.i & 1) != grp) continue;
+                if ((rt.i & 1) != grp) continue;
                 if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (!mbar_wait(tfree + 8 * rt.i, rt.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t st = base + (uint32_t)r.i * p.stage_bytes;
-#pragma unroll
-                for (int i = 0; i < kPer; i++) {
-                    const int pc = sub * kPer + i;
-                    const uint4 c = lds128(st + swizzled(kARow, row, pc));
-                    const int b = KB == 64 ? 2 * (kt & 1) + pc : pc & 3;
-                    const uint32_t word = lds32(st + so + (uint32_t)(pc >> 2) * 512u);
-                    uint32_t out[16];
-                    rebuild32(c, (word >> (8 * b)) & 255u, out);
-                    tmem_st16(tmem + p.a_col0 + (uint32_t)(KB / 2) * (uint32_t)rt.i + 16u * (uint32_t)pc +
-                                  ((uint32_t)(32 * quarter) << 16),
-                              out);
-                }
+                const uint4 c = lds128(st + sw32(row, pc));
+                const uint32_t word = lds32(st + so);
+                uint32_t out[16];
+                rebuild32(c, (word >> (16 * (kt & 1) + 8 * pc)) & 255u, out);
+                tmem_st16(tmem + p.a_col0 + (uint32_t)(KB / 2) * (uint32_t)rt.i + 16u * (uint32_t)pc + ((uint32_t)(32 * quarter) << 16),
+                          out);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -552,13 +668,14 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         const int row = warp * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t stg = base + p.stg_off;
-        const size_t slot_f4 = (size_t)(p.MG / 4) * kTileN;   // float4s of a CTA's partial
+        const size_t slot_f4 = (size_t)p.part_f4 * kTileN;   // float4s of a CTA's partial
         Walk wk(pl, blockIdx.x);
         Seg sg;
         Ring ra;
         while (wk.next(pl, p.kt, sg)) {
             const Tile t = locate(p, pl, sg.tile);
-            const int nN = (t.rows + 15) & ~15;
+            const int cols = (t.rows + 15) & ~15;
+            const uint32_t lo = (uint32_t)(mma_n<SRC>(t.rows) / 2);   // split rows: first lo column
             const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
             int last = blockIdx.x;
             if (joins) last = unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
@@ -568,13 +685,25 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             if (good) good = mbar_wait(accf + 8 * ra.i, ra.ph, p.timeout, abort_flag, 20000);
             if (any_of_epilogue(!good)) break;
             tc_fence_after();
-            const uint32_t acc = trow + (uint32_t)(ra.i * p.MG);
+            const uint32_t acc = trow + (uint32_t)ra.i * p.acc_w;
+            // 16 slots of the accumulator (hi + lo of split rows)
+            auto take = [&](int c, uint32_t (&v)[16]) {
+                tmem_ld16(acc + (uint32_t)c, v);
+                if (SRC == kGroupMx8) {
+                    uint32_t l[16];
+                    tmem_ld16(acc + lo + (uint32_t)c, l);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(l[i]));
+                } else {
+                    tmem_wait_ld();
+                }
+            };
             if (publish) {
                 float4* dst = reinterpret_cast<float4*>(p.partial) + (size_t)blockIdx.x * slot_f4 + row;
-                for (int c = 0; c < nN; c += 16) {
+                for (int c = 0; c < cols; c += 16) {
                     uint32_t v[16];
-                    tmem_ld16(acc + (uint32_t)c, v);
-                    tmem_wait_ld();
+                    take(c, v);
 #pragma unroll
                     for (int i = 0; i < 4; i++)
                         __stcg(dst + (size_t)(c / 4 + i) * kTileN,
@@ -589,15 +718,14 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                                  : "memory");
             } else {
                 const int64_t n0 = (int64_t)t.n * rows_a;
-                for (int c0 = 0; c0 < nN; c0 += kChunk) {
+                for (int c0 = 0; c0 < cols; c0 += kChunk) {
                     // accumulator (and the other ranges' partial sums, in k order) -> staging
 #pragma unroll
                     for (int hh = 0; hh < 2; hh++) {
                         const int c = c0 + 16 * hh;
-                        if (c >= nN) break;
+                        if (c >= cols) break;
                         uint32_t v[16];
-                        tmem_ld16(acc + (uint32_t)c, v);
-                        tmem_wait_ld();
+                        take(c, v);
                         for (int b = blockIdx.x + 1; b <= last; b++) {
                             const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)b * slot_f4 + row;
 #pragma unroll
@@ -685,65 +813,259 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     }
 }
 
-__global__ void __launch_bounds__(kThreadsPlain, 1)
-    k_group_bf16(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                 const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<kGroupBf16, 64>(tm_x, tm_w, tm_u, p);
-}
-
-__global__ void __launch_bounds__(kThreadsPlain, 1)
-    k_group_mx_mx(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                  const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<kGroupMxMx, 256>(tm_x, tm_w, tm_u, p);
+template <int SRC>
+__global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
+    k_group(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+            const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
+    group_body<SRC>(tm_x, tm_w, tm_u, p);
 }
 
 // 22 warps: 16 K registers of a sub-partition over six of them allow 80.
-template <int KB>
 __global__ void __maxnreg__(80)
-    k_group_mx(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-               const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<kGroupMx, KB>(tm_x, tm_w, tm_u, p);
+    k_group_rebuild(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
+    group_body<kGroupMx>(tm_x, tm_w, tm_u, p);
+}
+
+// ---------------------------------------------------------------- rows before the product
+struct PrepParams {
+    const uint16_t* X;
+    const int32_t* rows;      // NULL: slot s is row s
+    const int32_t* offsets;
+    int64_t x_rows, slots, K;
+    int E, MG, kt;
+    uint32_t sf_bytes;        // scale bytes in front of a stage's rows
+    int64_t chunk;
+    uint8_t* out;
+};
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepK = 512;   // k of a CTA: 16 a lane
+
+// Rows of split tiles: CTA (slot tile, 512 k); a warp takes a row at a time,
+// 16 values a lane, two lanes a block of 32.  Row r of a tile of n (rounded up
+// to 8) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
+// swizzled rows; their scale bytes lie in front as tcgen05.cp reads them.
+// Bound by reading the rows and writing as many bytes.
+__global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p) {
+    extern __shared__ int32_t tab[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int32_t* cum = tab;
+    int32_t* begin = cum + p.E + 1;
+    int32_t* count = begin + p.E;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) list_tiles(p.offsets, p.E, p.slots, p.MG, 1, cum, begin, count, lane);
+    __syncthreads();
+    if ((int)blockIdx.x >= cum[p.E]) return;
+    int e = 0;
+    for (int hi = p.E; hi - e > 1;) {
+        const int mid = (e + hi) >> 1;
+        if (cum[mid] <= (int)blockIdx.x) e = mid; else hi = mid;
+    }
+    const int m = (int)blockIdx.x - cum[e];
+    const int64_t s0 = (int64_t)begin[e] + (int64_t)m * p.MG;
+    const int nrows = count[e] - m * p.MG < p.MG ? count[e] - m * p.MG : p.MG;
+    const int n8 = (nrows + 7) & ~7;
+    const int64_t k = (int64_t)blockIdx.y * kPrepK + 16 * lane;
+    const bool in_k = k < p.K;   // K is a multiple of 128: the 8 lanes of a stage agree
+    uint8_t* out = p.out + ((int64_t)blockIdx.x * p.kt + k / 128) * p.chunk;
+    const int unit = lane & 7;   // 16-byte unit of the stage's row
+    for (int r = warp; r < nrows; r += kPrepThreads / 32) {
+        int64_t row = s0 + r;
+        if (p.rows) {
+            const int32_t v = p.rows[s0 + r];
+            const bool in = v >= 0 && v < p.x_rows;
+            if (!in) raise_status(UW_ERR_DEVICE);
+            row = in ? v : 0;
+        }
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (in_k) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k);
+            a = __ldg(src);
+            b = __ldg(src + 1);
+        }
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        float v[16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const uint32_t x = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+            if (x < 0x7F800000u) top = top > x ? top : x;
+            else v[i] = __uint_as_float(0x7FC00000u);   // e4m3 has no infinity: it becomes NaN, as its sums would
+        }
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+        top = top > other ? top : other;
+        // scale 2^s puts the largest into [2^7, 2^8); its byte also has to hold s - 4
+        const uint32_t ex = top >> 23;                        // floor(log2) + 127
+        const uint32_t sb = ex > 11u ? ex - 7u : 4u;          // s + 127
+        const float inv = __uint_as_float((254u - sb) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint32_t h2[2];
+            float d[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) d[j] = v[4 * i + j] * inv;
+            asm("{\n\t.reg .b16 x, y;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 x, %4, %3;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 y, %6, %5;\n\t"
+                "mov.b32 %0, {x, y};\n\t"
+                "cvt.rn.f16x2.e4m3x2 %1, x;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %2, y;\n\t}"
+                : "=r"(hi[i]), "=r"(h2[0]), "=r"(h2[1])
+                : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const __half2 h = *reinterpret_cast<const __half2*>(&h2[j]);
+                d[2 * j] = (d[2 * j] - __low2float(h)) * 16.0f;
+                d[2 * j + 1] = (d[2 * j + 1] - __high2float(h)) * 16.0f;
+            }
+            asm("{\n\t.reg .b16 x, y;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+                "mov.b32 %0, {x, y};\n\t}"
+                : "=r"(lo[i])
+                : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+        }
+        // the four scale bytes of the stage's row, in every lane of its eight
+        uint32_t sw = sb << (8 * (unit >> 1));
+        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
+        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
+        if (in_k) {
+            const int rh = r, rl = n8 + r;
+            uint8_t* body = out + p.sf_bytes;
+            *reinterpret_cast<uint4*>(body + rh * 128 + ((unit ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(body + rl * 128 + ((unit ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            auto at = [](int row) { return (row >> 7) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4; };
+            if (unit == 0) *reinterpret_cast<uint32_t*>(out + at(rh)) = sw;
+            if (unit == 1) *reinterpret_cast<uint32_t*>(out + at(rl)) = sw - 0x04040404u;
+        }
+    }
+}
+
+// Gathered copy: Xs[s] = X[rows[s]] for the slots of the groups, 16 bytes a
+// thread and step.
+__global__ void __launch_bounds__(kPrepThreads) k_group_gather(const PrepParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t first = p.offsets ? p.offsets[0] : 0, end = p.offsets ? p.offsets[p.E] : p.slots;
+    const int per = (int)(p.K / 8);   // 16-byte pieces of a row
+    const int64_t stop = end < p.slots ? end : p.slots;
+    for (int64_t s = (first > 0 ? first : 0) + blockIdx.x; s < stop; s += gridDim.x) {
+        const int32_t v = p.rows[s];
+        const bool in = v >= 0 && v < p.x_rows;
+        if (!in && threadIdx.x == 0) raise_status(UW_ERR_DEVICE);
+        const uint4* src = reinterpret_cast<const uint4*>(p.X + (in ? (int64_t)v : 0) * p.K);
+        uint4* dst = reinterpret_cast<uint4*>(p.out) + s * per;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < per; i += kPrepThreads) dst[i] = __ldg(src + i);
+    }
 }
 
 // Slots of a tile: twice the mean group (groups are uneven), a power of two
-// from 16 to 256.  Block-scaled products keep 128-slot scale tiles whole.
+// from 16 up.  At most 256; 112 split rows (two accumulators and the scales
+// fit tensor memory).  Block-scaled products keep 128-slot scale tiles whole.
 int pick_tile_slots(int src, int64_t slots, int E) {
     const int64_t groups = E < slots ? E : slots;
     const int64_t mean = (slots + groups - 1) / groups;
     const int64_t want = E == 1 ? mean : 2 * mean;
     int mg = src == kGroupMxMx ? 128 : 16;
     while (mg < 256 && mg < want) mg *= 2;
+    if (src == kGroupMx8 && mg > 64) mg = 112;
     return mg;
+}
+
+constexpr size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// How a call is cut up; the workspace holds partial sums, their tags, and the
+// prepared rows.
+struct Shape {
+    int MG = 0, KB = 0, kt = 0, n_tiles = 0;
+    int64_t m_tiles = 0;      // slot tiles at most
+    bool gather = false;      // a gathered copy of BF16 rows
+    uint32_t sf_b = 0;        // scale bytes of a stage's rows
+    int64_t chunk = 0;        // split rows: bytes of a stage
+    size_t partial = 0, flags = 0, prep = 0;
+    size_t bytes() const { return partial + flags + prep; }
+};
+
+Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, bool rows) {
+    Shape h;
+    const int P = num_sms();
+    h.MG = pick_tile_slots(src, slots, E);
+    h.KB = stage_k(src);
+    h.kt = (int)((K + h.KB - 1) / h.KB);
+    const int rows_a = up ? kTileN / 2 : kTileN;
+    h.n_tiles = (int)((N + rows_a - 1) / rows_a);
+    h.m_tiles = slots / h.MG + (E < slots ? E : slots);
+    h.partial = (size_t)P * h.MG * kTileN * 4;
+    h.flags = al256((size_t)P * 4 * 8);
+    if (src == kGroupMx8) {
+        h.sf_b = 512u * (uint32_t)((2 * h.MG + 127) / 128);
+        h.chunk = (int64_t)h.sf_b + 2 * h.MG * 128;
+        h.prep = al256((size_t)h.m_tiles * h.kt * h.chunk);
+    } else if (src == kGroupMxMx) {
+        h.sf_b = (uint32_t)(h.MG / kMxTileRows) * kMxTileBytes;
+    } else if (rows && h.MG > 32) {
+        h.gather = true;
+        h.prep = al256((size_t)slots * (size_t)K * 2);
+    }
+    return h;
+}
+
+// The unpacking TMA load takes rows of whole 128 codes.
+int resolve(int src, int64_t K) { return src == kGroupMx && K % 128 == 0 ? kGroupMx8 : src; }
+
+template <typename K, typename... A>
+cudaError_t launch_after(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-size_t group_ws_bytes(int src, int64_t slots, int E) {
-    if (slots <= 0) return 0;
-    const int P = num_sms(), mg = pick_tile_slots(src, slots, E);
-    return (size_t)P * mg * kTileN * 4 + (((size_t)P * 4 * 8 + 255) & ~size_t(255));
+size_t group_ws_bytes(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, bool rows) {
+    return slots <= 0 ? 0 : shape_of(resolve(src, K), slots, E, N, K, up, rows).bytes();
 }
 
 cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     *st = UW_OK;
     if (a.slots == 0) return cudaSuccess;
+    const int src = resolve(a.src, a.K);
+    const Shape h = shape_of(src, a.slots, a.E, a.N, a.K, a.up != nullptr, a.rows != nullptr);
+    const int MG = h.MG, P = num_sms();
+    const int64_t max_tiles = h.m_tiles * (int64_t)h.n_tiles;
+    if (max_tiles > 0x7FFFFFFF) { *st = UW_ERR_SHAPE; return cudaSuccess; }
+    if (!a.ws || a.ws_bytes < h.bytes()) { *st = UW_ERR_WORKSPACE; return cudaSuccess; }
+    uint8_t* prep = (uint8_t*)a.ws + h.partial + h.flags;
     GroupParams p{};
-    const int MG = pick_tile_slots(a.src, a.slots, a.E);
-    const int KB = a.src == kGroupBf16 ? 64 : a.src == kGroupMxMx ? 256 : MG <= 32 ? 256 : MG <= 128 ? 128 : 64;
     p.x_rows = a.x_rows;
     p.slots = a.slots;
     p.N = a.N;
-    p.rows = a.rows;
+    p.rows = src == kGroupMx8 || h.gather ? nullptr : a.rows;
     p.offsets = a.offsets;
     p.E = a.E;
-    p.kt = (int)((a.K + KB - 1) / KB);
+    p.kt = h.kt;
     p.MG = MG;
     p.box = MG < 64 ? MG : 64;
     p.up = a.up ? 1 : 0;
-    const int rows_a = p.up ? kTileN / 2 : kTileN;
-    p.n_tiles = (int)((a.N + rows_a - 1) / rows_a);
-    const int64_t max_tiles = ((a.slots + MG - 1) / MG + a.E) * (int64_t)p.n_tiles;
-    if (max_tiles > 0x7FFFFFFF) { *st = UW_ERR_SHAPE; return cudaSuccess; }
+    p.n_tiles = h.n_tiles;
     p.out_f32 = a.out_f32;
     p.y_vec = a.N % 8 == 0;
     p.Y = a.Y;
@@ -752,41 +1074,40 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.sx = a.x_scales;
     p.w_row_tiles = mx_row_tiles(a.N);
     p.k_tiles = (int)mx_k_tiles(a.K);
-    const int P = num_sms();
-    if (!a.ws || a.ws_bytes < group_ws_bytes(a.src, a.slots, a.E)) { *st = UW_ERR_WORKSPACE; return cudaSuccess; }
+    p.early = src == kGroupMx8 || h.gather;
+    p.prep = prep;
+    p.prep_chunk = h.chunk;
+    p.part_f4 = MG / 4;
     p.partial = (float*)a.ws;
-    p.flags = (unsigned long long*)((uint8_t*)a.ws + (size_t)P * MG * kTileN * 4);
+    p.flags = (unsigned long long*)((uint8_t*)a.ws + h.partial);
     p.epoch = gemm_next_epoch();
     p.timeout = timeout_ns();
 
-    // stage: weight rows, scale bytes, X (every swizzled tile 1024-byte aligned)
+    // stage: weight rows, their scales, the rows' scales, X (swizzled tiles 1024-byte aligned)
     auto al1k = [](uint32_t x) { return (x + 1023u) & ~1023u; };
-    const uint32_t a_row = a.src == kGroupBf16 ? 128 : KB / 2;
-    const int halves = a.src == kGroupMxMx ? 1 : KB / 64;
-    p.off_s = kTileN * a_row;
-    p.sf_a_bytes = a.src == kGroupBf16 ? 0 : KB == 256 ? kMxTileBytes : kMxTileBytes / 2;
-    p.sf_b_bytes = a.src == kGroupMxMx ? (uint32_t)(MG / kMxTileRows) * kMxTileBytes : 0;
-    p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up ? 2 : 1) + p.sf_b_bytes);
-    p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * halves);
+    p.off_s = kTileN * (src == kGroupMx ? 32u : 128u);
+    p.sf_a_bytes = src == kGroupBf16 ? 0 : src == kGroupMxMx ? kMxTileBytes : kMxTileBytes / 2;
+    p.sf_b_bytes = h.sf_b;
+    // (with `up`, split rows: a third part for the joined scales of both weights)
+    p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up ? (src == kGroupMx8 ? 3 : 2) : 1) + p.sf_b_bytes);
+    p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1));
     const uint32_t ctrl = 512, tab = (uint32_t)(3 * a.E + 1) * 4;
     const uint32_t fixed = 1024 + ctrl + kStage32 + ((tab + 15u) & ~15u);
-    // tensor memory: accumulators, then rebuilt-A slots (KB/2 columns) or scale columns
-    const uint32_t per_slot = a.src == kGroupMx ? KB / 2 : a.src == kGroupMxMx ? 8 + 8 * (MG / kMxTileRows) : 0;
-    p.nacc = a.src == kGroupBf16 || 2 * MG <= 256 ? 2 : 1;
-    const uint32_t acc_cols = (uint32_t)(p.nacc * MG);
+    // tensor memory: accumulators, then rebuilt-A slots (32 columns) or scale columns
+    p.acc_w = (uint32_t)(src == kGroupMx8 ? 2 * MG : MG);
+    p.sf_slot = src == kGroupMxMx ? 8u + 8u * (uint32_t)(MG / kMxTileRows) : src == kGroupMx8 ? 4u + h.sf_b / 128u : 0u;
+    p.nacc = src == kGroupBf16 || src == kGroupMx8 || 2 * MG <= 256 ? 2 : 1;
+    const uint32_t acc_cols = (uint32_t)p.nacc * p.acc_w;
     int S = (int)((227 * 1024 - fixed) / p.stage_bytes);
     if (S > kMaxS) S = kMaxS;
-    if (a.src == kGroupMxMx && S > (int)((kTmemCols - acc_cols) / per_slot)) S = (int)((kTmemCols - acc_cols) / per_slot);
-    p.T = 0;
-    if (a.src == kGroupMx) {
-        p.T = (int)((kTmemCols - acc_cols) / per_slot);
+    if (p.sf_slot && S > (int)((kTmemCols - acc_cols) / p.sf_slot)) S = (int)((kTmemCols - acc_cols) / p.sf_slot);
+    if (src == kGroupMx) {
+        p.T = (int)((kTmemCols - acc_cols) / 32u);
         if (p.T > kMaxT) p.T = kMaxT;
-        if (KB == 64) {   // two rebuild groups: even rings
-            S &= ~1;
-            p.T &= ~1;
-        }
+        S &= ~1;   // two rebuild groups: even rings
+        p.T &= ~1;
     }
-    if (S < 2 || (a.src == kGroupMx && p.T < 2)) { *st = UW_ERR_UNSUPPORTED; return cudaSuccess; }
+    if (S < 2 || (src == kGroupMx && p.T < 2)) { *st = UW_ERR_UNSUPPORTED; return cudaSuccess; }
     p.S = S;
     p.a_col0 = p.sf_col0 = acc_cols;
     p.ctrl_off = (uint32_t)S * p.stage_bytes;
@@ -795,48 +1116,60 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     const size_t smem = (size_t)S * p.stage_bytes + fixed;
 
     CUtensorMap tx{}, tw{}, tu{};
-    bool ok;
+    bool ok = true;
     const uint64_t wrows = (uint64_t)a.E * (uint64_t)a.N;
-    if (a.src == kGroupMxMx)
+    if (src == kGroupMxMx)
         ok = make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, a.K / 2, a.x_rows, a.K / 2, 128, p.box,
                          CU_TENSOR_MAP_SWIZZLE_128B);
-    else
-        ok = make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, a.K, a.x_rows, a.K * 2, 64, a.rows ? 1 : p.box,
-                         CU_TENSOR_MAP_SWIZZLE_128B);
-    for (int h = 0; h < 2; h++) {
-        const void* w = h && a.up ? a.up : a.W;
-        CUtensorMap* m = h ? &tu : &tw;
-        if (a.src == kGroupBf16)
+    else if (src != kGroupMx8)
+        ok = make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.gather ? (const void*)prep : a.X, a.K,
+                         h.gather ? a.slots : a.x_rows, a.K * 2, 64, p.rows ? 1 : p.box, CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < 2; i++) {
+        const void* w = i && a.up ? a.up : a.W;
+        CUtensorMap* m = i ? &tu : &tw;
+        if (src == kGroupBf16)
             ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, a.K, wrows, a.K * 2, 64, kTileN / 2,
                                    CU_TENSOR_MAP_SWIZZLE_128B);
+        else if (src == kGroupMx8)   // 16 packed codes -> 16 bytes of shared memory
+            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 1, w, a.K, wrows, a.K / 2, 128, kTileN / 2,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
         else
-            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.K / 2, wrows, a.K / 2, a_row, kTileN / 2,
-                                   KB == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                   : KB == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                               : CU_TENSOR_MAP_SWIZZLE_32B);
+            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.K / 2, wrows, a.K / 2, src == kGroupMx ? 32 : 128,
+                                   kTileN / 2, src == kGroupMx ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (!ok) { *st = UW_ERR_CUDA; return cudaSuccess; }
+    if (src == kGroupMx8) tx = tw;   // unused
 
     void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupParams) =
-        a.src == kGroupBf16   ? k_group_bf16
-        : a.src == kGroupMxMx ? k_group_mx_mx
-        : KB == 256           ? k_group_mx<256>
-        : KB == 128           ? k_group_mx<128>
-                              : k_group_mx<64>;
+        src == kGroupBf16   ? k_group<kGroupBf16>
+        : src == kGroupMxMx ? k_group<kGroupMxMx>
+        : src == kGroupMx8  ? k_group<kGroupMx8>
+                            : k_group_rebuild;
     cudaError_t e = set_smem_attr((const void*)kern, (int)smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(max_tiles * p.kt < P ? max_tiles * p.kt : P));
-    cfg.blockDim = dim3(a.src == kGroupMx ? kThreadsRebuild : kThreadsPlain);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tx, tw, tu, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+
+    if (p.early) {
+        PrepParams q{};
+        q.X = (const uint16_t*)a.X;
+        q.rows = a.rows;
+        q.offsets = a.offsets;
+        q.x_rows = a.x_rows;
+        q.slots = a.slots;
+        q.K = a.K;
+        q.E = a.E;
+        q.MG = MG;
+        q.kt = h.kt;
+        q.sf_bytes = h.sf_b;
+        q.chunk = h.chunk;
+        q.out = prep;
+        if (src == kGroupMx8)
+            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK)), kPrepThreads, tab, s, q);
+        else
+            e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), kPrepThreads, 0, s, q);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(kern, dim3((unsigned)(max_tiles * h.kt < P ? max_tiles * h.kt : P)),
+                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 ? kThreadsMix : kThreadsPlain, smem, s, tx, tw, tu, p);
 }
 
 }  // namespace uw

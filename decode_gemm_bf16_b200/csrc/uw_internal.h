@@ -225,7 +225,9 @@ cudaError_t launch_combine(const void* Z, int in_f32, int64_t slots, const int32
                            int k, int64_t N, void* Y, int out_f32, cudaStream_t s);
 
 // ---- products of ragged groups (uw_group.cu)
-enum GroupSource { kGroupBf16 = 0, kGroupMx = 1, kGroupMxMx = 2 };
+// kGroupMx8: 4-bit weights against rows split in two e4m3 halves (what kGroupMx
+// becomes where K allows it)
+enum GroupSource { kGroupBf16 = 0, kGroupMx = 1, kGroupMxMx = 2, kGroupMx8 = 3 };
 struct GroupGemm {
     int src = kGroupBf16;
     const void* X = nullptr;             // BF16 [x_rows, K], or codes (kGroupMxMx)
@@ -245,7 +247,7 @@ struct GroupGemm {
     void* ws = nullptr;
     size_t ws_bytes = 0;
 };
-size_t group_ws_bytes(int src, int64_t slots, int E);
+size_t group_ws_bytes(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, bool rows);
 cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st);
 
 }  // namespace uw

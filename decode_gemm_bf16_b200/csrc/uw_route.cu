@@ -27,8 +27,9 @@ int route_status_take() { return unit_status_take(); }
 
 namespace {
 
-constexpr int kRouteThreads = 512;
+constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRankWarps = 16;   // warps that rank choices (a row of counts each)
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 struct RouteParams {
@@ -93,13 +94,16 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
     for (int j = 0; j < p.k; j++) {
         const uint32_t mx = __reduce_max_sync(kFull, best);
         if (mx == 0) break;
+        // the lowest index among the lanes that hold it: mostly one lane, no second reduction
+        const uint32_t holders = __ballot_sync(kFull, best == mx);
         uint32_t cand = 0xFFFFFFFFu;
         if (best == mx) {
 #pragma unroll
             for (int i = VPL - 1; i >= 0; i--)
                 if (key[i] == mx) cand = (uint32_t)(32 * i + lane);
         }
-        const uint32_t e = __reduce_min_sync(kFull, cand);
+        const uint32_t e = (holders & (holders - 1)) == 0 ? __shfl_sync(kFull, cand, __ffs(holders) - 1)
+                                                          : __reduce_min_sync(kFull, cand);
         if (cand == e) {   // this lane held it
             best = 0;
 #pragma unroll
@@ -128,7 +132,7 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
     int32_t* base = sm;
     int32_t* total = sm + E;
     int32_t* wcount = total + E + 1;
-    for (int i = tid; i < 2 * E + 1 + kRouteWarps * E; i += kRouteThreads) sm[i] = 0;
+    for (int i = tid; i < 2 * E + 1 + kRankWarps * E; i += kRouteThreads) sm[i] = 0;
     __syncthreads();
     // counts of the CTAs before this one, and of all: the threads cover E
     // experts times as many row groups as fit
@@ -152,9 +156,10 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
     const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
     const int64_t first = t0 * p.k;
     const int64_t n = t1 > t0 ? (t1 - t0) * p.k : 0;
-    const int64_t per = ((n + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
-    const int64_t w0 = first + (per * warp < n ? per * warp : n), w1 = first + (per * (warp + 1) < n ? per * (warp + 1) : n);
-    int32_t* mine = wcount + warp * E;
+    const int64_t per = ((n + kRankWarps - 1) / kRankWarps + 31) / 32 * 32;
+    const int64_t lo = warp < kRankWarps ? per * warp : n, hi = warp < kRankWarps ? per * (warp + 1) : n;
+    const int64_t w0 = first + (lo < n ? lo : n), w1 = first + (hi < n ? hi : n);
+    int32_t* mine = wcount + (warp < kRankWarps ? warp : 0) * E;
     for (int64_t i = w0 + lane; i < w1; i += 32) {
         const int e = p.ids[i];
         if (e >= 0) atomicAdd(&mine[e], 1);
@@ -182,7 +187,7 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
     __syncthreads();
     for (int e = tid; e < E; e += kRouteThreads) {
         int at = total[e] + base[e];
-        for (int w = 0; w < kRouteWarps; w++) {
+        for (int w = 0; w < kRankWarps; w++) {
             const int c = wcount[w * E + e];
             wcount[w * E + e] = at;
             at += c;
@@ -291,30 +296,43 @@ struct CombineParams {
     void* Y;
 };
 
+// 8 columns as loaded: BF16 in the first vector, fp32 in both.
 template <bool F32>
-__device__ __forceinline__ void load_cols(const void* Z, int64_t at, int n, bool vec, float (&v)[8]) {
+struct Cols {
+    uint4 a, b;
+};
+
+template <bool F32>
+__device__ __forceinline__ void load_cols(const void* Z, int64_t at, int n, bool vec, Cols<F32>& r) {
     if (vec) {
-        if (F32) {
-            const float4* z = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(Z) + at);
-            const float4 a = __ldg(z), b = __ldg(z + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(Z) + at));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        }
+        const uint4* z = F32 ? reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(Z) + at)
+                             : reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(Z) + at);
+        r.a = __ldcs(z);
+        if (F32) r.b = __ldcs(z + 1);
     } else {
+        uint32_t w[8] = {};
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[i] = 0.0f;
-            if (i < n)
-                v[i] = F32 ? reinterpret_cast<const float*>(Z)[at + i]
-                           : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(Z)[at + i] << 16);
+        for (int i = 0; i < 8; i++)
+            if (i < n) {
+                if (F32) w[i] = reinterpret_cast<const uint32_t*>(Z)[at + i];
+                else w[i >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(Z)[at + i] << (16 * (i & 1));
+            }
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        if (F32) r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void add_cols(const Cols<F32>& r, float w, float (&acc)[8]) {
+    const uint32_t a[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, b[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (F32) {
+            acc[i] = fmaf(w, __uint_as_float(a[i]), acc[i]);
+            acc[4 + i] = fmaf(w, __uint_as_float(b[i]), acc[4 + i]);
+        } else {
+            acc[2 * i] = fmaf(w, __uint_as_float(a[i] << 16), acc[2 * i]);
+            acc[2 * i + 1] = fmaf(w, __uint_as_float(a[i] & 0xFFFF0000u), acc[2 * i + 1]);
         }
     }
 }
@@ -322,7 +340,7 @@ __device__ __forceinline__ void load_cols(const void* Z, int64_t at, int n, bool
 // Rows of N values are 16-byte aligned runs of 8 columns when N % 8 == 0;
 // otherwise every value is loaded and stored by itself.
 template <bool IN32, bool OUT32>
-__global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineParams p) {
+__global__ void __launch_bounds__(kCombineThreads, IN32 ? 2 : 4) k_combine(const CombineParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
@@ -332,11 +350,12 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineParams
     const int n = p.N - c < 8 ? (int)(p.N - c) : 8;
     float acc[8] = {};
     for (int j0 = 0; j0 < p.k; j0 += kCombineAhead) {
-        float z[kCombineAhead][8], w[kCombineAhead];
+        Cols<IN32> z[kCombineAhead];
+        float w[kCombineAhead];
 #pragma unroll
         for (int j = 0; j < kCombineAhead; j++) {
-            w[j] = 0.0f;
             int32_t s = -1;
+            w[j] = 0.0f;
             if (j0 + j < p.k) {
                 s = __ldg(p.pos + t * p.k + j0 + j);
                 w[j] = __ldg(p.weights + t * p.k + j0 + j);
@@ -345,18 +364,12 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineParams
                 raise_status(UW_ERR_DEVICE);
                 s = -1;
             }
-            if (s >= 0) {
-                load_cols<IN32>(p.Z, s * p.N + c, n, vec, z[j]);
-            } else {
-                w[j] = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 8; q++) z[j][q] = 0.0f;
-            }
+            z[j].a = z[j].b = make_uint4(0, 0, 0, 0);
+            if (s >= 0) load_cols<IN32>(p.Z, s * p.N + c, n, vec, z[j]);
+            else w[j] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < kCombineAhead; j++)
-#pragma unroll
-            for (int q = 0; q < 8; q++) acc[q] = fmaf(w[j], z[j][q], acc[q]);
+        for (int j = 0; j < kCombineAhead; j++) add_cols<IN32>(z[j], w[j], acc);
     }
     const int64_t at = t * p.N + c;
     if (OUT32) {
@@ -417,7 +430,7 @@ cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k
     p.rows = rows;
     p.pos = pos;
     p.hist = hist;
-    const size_t smem = (size_t)(2 * E + 1 + kRouteWarps * E) * 4;
+    const size_t smem = (size_t)(2 * E + 1 + kRankWarps * E) * 4;
     const RouteKernel choose_k = in_f32 ? route_kernel<true>(E) : route_kernel<false>(E);
     const size_t smem_c = ctas == 1 ? smem : (size_t)E * 4;
     cudaError_t e = smem_c > 48 * 1024 ? set_smem_attr((const void*)choose_k, (int)smem_c) : cudaSuccess;

@@ -390,7 +390,7 @@ uw_status uw_gemm_direct_palette_noalloc(const uint16_t* X, int64_t M, const uw_
  *     Bytes of rows and blocks past the matrix are 0 (uw_mx_quantize writes
  *     them; whoever builds the plane by hand does the same).
  * K is a positive multiple of 64, rows * K at most 2^31 - 256 per matrix, as
- * everywhere.  Pointers are 16-byte aligned. */
+ * everywhere.  Codes are 32-byte aligned, other pointers 16-byte. */
 typedef struct {
     const uint8_t* codes;    /* device, uw_mx_bytes' code_bytes                              */
     const uint8_t* scales;   /* device, uw_mx_bytes' scale_bytes                             */
@@ -411,8 +411,13 @@ uw_status uw_mx_dequantize(const uw_mx_matrix* m, void* out, int out_f32, void* 
 
 /* Y[M,N] = X[M,K] . W^T with W one MXFP4 matrix [N, K] (batch 1), accumulated
  * in float32 on the tensor cores and rounded once.  Exactly one of X, X_mx:
- *   X: device BF16 [M,K]; the weights are rebuilt to BF16 on chip, which is
- *     exact wherever BF16 holds the value.
+ *   X: device BF16 [M,K].  With K a multiple of 128 each value enters the
+ *     8-bit tensor cores as 2^s (hi + lo/16), 2^s the scale of its block of 32
+ *     along K: exactly, if it is at least 2^-13 times the block's largest;
+ *     below, off by at most 2^-21 of that largest (2^-137 in a block whose
+ *     largest is below 2^-115).
+ *     An infinity in X counts as NaN.  With other K the weights are rebuilt to
+ *     BF16 on chip, exactly wherever BF16 holds the value.
  *   X_mx: MXFP4 [M,K] (batch 1; M = its rows): block-scaled 4-bit products.
  * Y: device [M,N], BF16 or float32 (out_f32), 16-byte aligned.  M = 0 is a
  * no-op.  workspace: 256-byte aligned, any contents, owned by the call until
@@ -461,11 +466,12 @@ uw_status uw_route(const void* logits, int in_f32, int64_t T, int E, int k, int 
  *     s; x_rows >= slots) or the row of each slot, device int32[slots].
  *   offsets: device int32[E + 1], not falling, at most `slots`; rows of Y at
  *     or past offsets[E] (and before offsets[0]) are left as they were.
- *     Offsets that fall or pass `slots`, or a row index outside [0, x_rows) in
- *     a group, raise UW_ERR_DEVICE in the device status word; the rows
- *     concerned are unspecified, no access leaves the buffers.
- *   W / up: device BF16 [E, N, K], or W_mx / up_mx: MXFP4 (batch E, rows N).
- *     Both of one kind.  E <= 1024, E * N <= 2^31 - 256.
+ *     Offsets that fall or pass `slots` raise UW_ERR_DEVICE in the device
+ *     status word, and nothing is computed.  A row index outside [0, x_rows)
+ *     in a group raises it too; that slot's outputs are unspecified.  No
+ *     access leaves the buffers.
+ *   W / up: device BF16 [E, N, K], or W_mx / up_mx: MXFP4 (batch E, rows N;
+ *     values of X as in uw_mx_gemm).  Both of one kind.  E <= 1024, E * N <= 2^31 - 256.
  *   Y: device [slots, N], BF16 or float32 (out_f32), 16-byte aligned.
  *   workspace: 256-byte aligned, any contents, owned by the call until it
  *     completes (a captured call owns it whenever its graph runs). */
@@ -487,8 +493,7 @@ typedef struct {
     size_t workspace_bytes;
 } uw_group_args;
 
-/* Reads slots, E, N, K and which weights are given; pointers may be NULL
- * otherwise. */
+/* Reads slots, E, N, K, which weights are given and whether rows is. */
 uw_status uw_gemm_grouped_workspace(const uw_group_args* args, size_t* bytes);
 
 uw_status uw_gemm_grouped(const uw_group_args* args, void* stream);

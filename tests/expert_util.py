@@ -87,6 +87,12 @@ def product_tolerance(absolute: torch.Tensor, K: int) -> torch.Tensor:
     return K * 2.0 ** -23 * absolute
 
 
+def split_tolerance(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
+    """BF16 rows against 4-bit weights: a value may enter the product off by 2^-21 of the largest of its block of 32."""
+    top = X.abs().unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1)
+    return 2.0 ** -21 * (top @ W.abs().T)
+
+
 def swiglu_ref(g: torch.Tensor, u: torch.Tensor) -> torch.Tensor:
     return g * torch.sigmoid(g) * u
 
@@ -106,16 +112,17 @@ def check(y: torch.Tensor, ref: torch.Tensor, tol: torch.Tensor):
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside; first at {bad.nonzero()[0].tolist()}, worst {float((err / tol).nan_to_num(1e9).max()):.3g}x"
 
 
-def grouped_ref(X, W, offsets, rows, up):
+def grouped_ref(X, W, offsets, rows, up, mx):
     """(reference, tolerance) over the slots inside the offsets; X, W, up in float64."""
     ys, ts = [], []
     K = X.shape[1]
     for e in range(W.shape[0]):
         lo, hi = int(offsets[e]), int(offsets[e + 1])
         x = X[lo:hi] if rows is None else X[rows[lo:hi].long()]
-        g, dg = x @ W[e].T, product_tolerance(x.abs() @ W[e].abs().T, K)
+        part = lambda w: (x @ w.T, product_tolerance(x.abs() @ w.abs().T, K) + (split_tolerance(x, w) if mx else 0))  # noqa: E731
+        g, dg = part(W[e])
         if up is not None:
-            u, du = x @ up[e].T, product_tolerance(x.abs() @ up[e].abs().T, K)
+            u, du = part(up[e])
             ys.append(swiglu_ref(g, u))
             ts.append(swiglu_tolerance(g, u, dg, du))
         else:

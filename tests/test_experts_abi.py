@@ -55,6 +55,7 @@ def test_mx_refusals(L):
     q = L.uw_mx_quantize
     assert q(None, 0, 1, 4, 64, A, A, None) == 1 and q(A, 0, 1, 4, 64, None, A, None) == 1
     assert q(A + 2, 0, 1, 4, 64, A, A, None) == 1 and q(A, 0, 1, 4, 64, A, A + 8, None) == 1
+    assert q(A, 0, 1, 4, 64, A + 16, A, None) == 1
     assert q(A, 0, 1, 4, 100, A, A, None) == 2
     assert q(None, 0, 1, 0, 64, None, None, None) == 0 and q(None, 0, 0, 4, 64, None, None, None) == 0
     d = L.uw_mx_dequantize

@@ -120,6 +120,8 @@ def test_mx_gemm(N, K, M, xmx):
     Xv = (uw.uw_mx_dequantize(Xq, out_f32=True) if xmx else X).double()
     Wv = uw.uw_mx_dequantize(W, out_f32=True).double()
     ref, tol = Xv @ Wv.T, U.product_tolerance(Xv.abs() @ Wv.abs().T, K)
+    if not xmx:
+        tol = tol + U.split_tolerance(Xv, Wv)
     for f32 in (False, True):
         out = torch.full((M, N), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
         y = uw.uw_mx_gemm(Xq, W, out=out, out_f32=f32)
@@ -136,7 +138,8 @@ def test_mx_gemm_full_size(M, xmx):
     Xq = uw.uw_mx_quantize(X) if xmx else X
     Xv = (uw.uw_mx_dequantize(Xq, out_f32=True) if xmx else X).double()
     Wv = uw.uw_mx_dequantize(W, out_f32=True).double()
-    U.check(uw.uw_mx_gemm(Xq, W), Xv @ Wv.T, U.product_tolerance(Xv.abs() @ Wv.abs().T, K))
+    tol = U.product_tolerance(Xv.abs() @ Wv.abs().T, K)
+    U.check(uw.uw_mx_gemm(Xq, W), Xv @ Wv.T, tol if xmx else tol + U.split_tolerance(Xv, Wv))
 
 
 @pytest.mark.parametrize("xmx", [False, True])
@@ -162,6 +165,31 @@ def test_mx_gemm_scale_extremes(xmx):
     assert y2[:, 5].isnan().all()
     y2[:, 5] = y[:, 5]
     assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("K", [128, 320, 1024])
+def test_mx_gemm_rows_of_wide_range(K):
+    """Values from 2^-30 to 2^30 in one block, outlier channels, rows near the ends of the range; NaN and infinity stay in their row."""
+    N, M = 130, 24
+    X = torch.randn(M, K, generator=_gen(1), device="cuda") * torch.exp2(torch.randint(-30, 31, (M, K), generator=_gen(2), device="cuda").float())
+    X[3] = torch.randn(K, generator=_gen(3), device="cuda") * 2.0 ** 100
+    X[4] = torch.randn(K, generator=_gen(4), device="cuda") * 2.0 ** -100
+    X[5] = 0
+    X[6, ::32] = 2.0 ** 110
+    X = X.to(torch.bfloat16)
+    W = uw.uw_mx_quantize(_bf16(N, K, seed=N, scale=0.02))
+    Xv, Wv = X.double(), uw.uw_mx_dequantize(W, out_f32=True).double()
+    tol = U.product_tolerance(Xv.abs() @ Wv.abs().T, K) + U.split_tolerance(Xv, Wv) + 1e-38
+    y = uw.uw_mx_gemm(X, W, out_f32=True)
+    U.check(y, Xv @ Wv.T, tol)
+    X[7, 5], X[8, 40], X[9, 70] = math.nan, math.inf, -math.inf
+    z = uw.uw_mx_gemm(X, W, out_f32=True)
+    for r in range(M):
+        if r in (7, 8, 9):
+            w = Wv[:, {7: 5, 8: 40, 9: 70}[r]]
+            assert not z[r][w != 0].isfinite().any()
+        else:
+            assert torch.equal(y[r], z[r])
 
 
 # ---------------------------------------------------------------- router
@@ -253,7 +281,7 @@ def _grouped_case(sizes, N, K, mx, up, gather, seed=0, T=None):
     X = _bf16(T, K, seed=seed)
     rows = torch.randint(0, T, (R,), generator=_gen(seed), device="cuda").int() if gather else None
     off = _offsets(sizes)
-    ref, tol = U.grouped_ref(X.double(), Wv[0], off.cpu(), rows, Wv[1] if up else None)
+    ref, tol = U.grouped_ref(X.double(), Wv[0], off.cpu(), rows, Wv[1] if up else None, mx)
     return X, W, off, rows, ref, tol
 
 
@@ -323,7 +351,7 @@ def test_grouped_bad_offsets_and_rows_are_reported():
 @pytest.mark.parametrize("fill", [0x00, 0xFF, "random"])
 def test_grouped_workspace_contents_do_not_matter(mx, fill):
     X, W, off, rows, ref, tol = _grouped_case([3, 2, 1], 400, 2048, mx, True, True)
-    n = uw.uw_gemm_grouped_workspace(6, W[0], W[1])
+    n = uw.uw_gemm_grouped_workspace(6, W[0], W[1], gathered=True)
     ws = (torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda") if fill == "random"
           else torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
     for _ in range(3):
@@ -388,11 +416,13 @@ def _layer_ref(x, ws, mx, r):
             xs = x[t:t + 1].double()
             g, u = xs @ v[0][e].T, xs @ v[1][e].T
             h = U.swiglu_ref(g, u)
-            dg, du = (U.product_tolerance(xs.abs() @ w.abs().T, K) for w in (v[0][e], v[1][e]))
+            dg, du = (U.product_tolerance(xs.abs() @ w.abs().T, K) + (U.split_tolerance(xs, w) if mx else 0) for w in (v[0][e], v[1][e]))
             dh = U.swiglu_tolerance(g, u, dg, du)
             dh = dh + 2.0 ** -8 * (h.abs() + dh)                          # h is rounded to BF16
             z = h @ v[2][e].T
             dz = dh @ v[2][e].abs().T + U.product_tolerance((h.abs() + dh) @ v[2][e].abs().T, h.shape[1])
+            if mx:
+                dz = dz + U.split_tolerance(h.abs() + dh, v[2][e])
             dz = dz + 2.0 ** -8 * (z.abs() + dz)                          # so is z
             w = float(r.weights[t, j])
             y[t] += w * z[0]
