@@ -715,10 +715,12 @@ def uw_route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool 
         i32 = dict(dtype=torch.int32, device=device)
         r = Route(torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device=device), torch.empty(E + 1, **i32),
                   torch.empty(T * k, **i32), torch.empty(T, k, **i32))
-        ws = _scratch(ws, need, device)
+        if ws is not None or need:
+            ws = _scratch(ws, need, device)
         _check(lib().uw_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, T, E, int(k), SCORES[score],
                               1 if renorm else 0, float(scale), r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
-                              r.rows.data_ptr(), r.pos.data_ptr(), ws.data_ptr(), ws.numel(), handle), "uw_route")
+                              r.rows.data_ptr(), r.pos.data_ptr(), ws.data_ptr() if ws is not None else None,
+                              ws.numel() if ws is not None else 0, handle), "uw_route")
     return r
 
 

@@ -45,7 +45,11 @@ uw_status check_route(int64_t T, int E, int k) {
     return UW_OK;
 }
 
-size_t route_ws_bytes(int64_t T, int E, int k) { return T ? ((size_t)route_blocks(T, k) * E * 4 + 255) & ~size_t(255) : 0; }
+// One CTA needs none.
+size_t route_ws_bytes(int64_t T, int E, int k) {
+    const int b = T ? route_blocks(T, k) : 0;
+    return b > 1 ? ((size_t)b * E * 4 + 255) & ~size_t(255) : 0;
+}
 
 uw_status check_group(const uw_group_args* a, int* src) {
     if (!a || a->slots < 0 || a->E < 1) return UW_ERR_INVALID_ARG;
@@ -158,7 +162,8 @@ extern "C" uw_status uw_route(const void* logits, int in_f32, int64_t T, int E, 
     if (!logits || !ids || !weights || !rows || !pos) return UW_ERR_INVALID_ARG;
     if (!aligned(logits, in_f32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(rows, 4) || !aligned(pos, 4))
         return UW_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < route_ws_bytes(T, E, k)) return UW_ERR_WORKSPACE;
+    const size_t need = route_ws_bytes(T, E, k);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return UW_ERR_WORKSPACE;
     return cuda_ok(launch_route(logits, in_f32, T, E, k, score, renorm ? 1 : 0, scale, ids, weights, offsets, rows, pos,
                                 (int32_t*)workspace, (cudaStream_t)stream));
 }

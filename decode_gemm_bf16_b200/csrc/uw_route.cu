@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRankWarps = 16;   // warps that rank choices (a row of counts each)
+constexpr int kRankWarps = kRouteWarps;   // warps that rank choices (a row of counts each)
 constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kSingle = 512;     // choices up to which one CTA does everything
 
 struct RouteParams {
     const void* logits;
@@ -46,12 +47,6 @@ struct RouteParams {
     int32_t* hist;   // [CTAs][E]
 };
 
-// Order-preserving key of a logit; 0: never chosen (NaN, -infinity).
-__device__ __forceinline__ uint32_t logit_key(float x) {
-    x = fminf(x, 3.402823466e38f) + 0.0f;   // +inf -> largest finite, -0 -> 0 (a NaN becomes the largest finite: see the caller)
-    const uint32_t b = __float_as_uint(x);
-    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
 __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
@@ -62,61 +57,123 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One token: lane j < k ends up with choice j (expert id, or -1) and weight.
+// Logits of token t, expert 32 i + lane, as fp32 bits (NaN past E); all loads
+// are issued before any is used.
 template <int VPL, bool F32>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& id, float& w) {
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, uint32_t (&raw)[VPL]) {
+    if (F32) {
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + lane;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) raw[i] = 32 * i + lane < p.E ? __ldg(x + 32 * i) : 0x7FC00000u;
+    } else {
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(p.logits) + t * p.E + lane;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) raw[i] = 32 * i + lane < p.E ? (uint32_t)__ldg(x + 32 * i) : 0x7FC0u;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) raw[i] <<= 16;
+    }
+}
+
+// Order-preserving key of a logit's bits; 0: never chosen (NaN, -infinity).
+// +infinity counts as the largest finite number, -0 as 0.
+__device__ __forceinline__ uint32_t bits_key(uint32_t b) {
+    if (b == 0x7F800000u) b = 0x7F7FFFFFu;
+    if (b == 0x80000000u) b = 0;
+    const bool out = (b & 0x7FFFFFFFu) > 0x7F800000u || b == 0xFF800000u;
+    return out ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// The k largest keys in falling order, equal keys by index: lane j < k ends up
+// with choice j.  k rounds of a maximum over the warp and a minimum over the
+// indices that reach it.
+template <int VPL>
+__device__ __noinline__ uint2 select_exact(const RouteParams& p, int64_t t, int lane) {
     uint32_t key[VPL];
+    load_logits<VPL, true>(p, t, lane, key);
 #pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = 32 * i + lane;
-        key[i] = 0;
-        if (e < p.E) {
-            const float x = F32 ? reinterpret_cast<const float*>(p.logits)[t * p.E + e]
-                                : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.logits)[t * p.E + e] << 16);
-            if (x == x && x != -INFINITY) key[i] = logit_key(x);
-        }
-    }
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; i++) best = best > key[i] ? best : key[i];
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    // softmax over every logit: the denominator, before keys are taken out
-    float total = 0.0f;
-    const float m = key_logit(top);   // top = 0 (no choice at all): unused
-    if (p.score == UW_SCORE_SOFTMAX && !p.renorm && top) {
-#pragma unroll
-        for (int i = 0; i < VPL; i++)
-            if (key[i]) total += expf(key_logit(key[i]) - m);
-        total = warp_sum(total);
-    }
-    id = -1;
-    uint32_t mine = 0;
+    for (int i = 0; i < VPL; i++) key[i] = bits_key(key[i]);
+    uint2 mine = make_uint2(0xFFFFFFFFu, 0);   // (expert, key)
     for (int j = 0; j < p.k; j++) {
+        uint32_t best = 0, cand = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) best = best > key[i] ? best : key[i];
         const uint32_t mx = __reduce_max_sync(kFull, best);
         if (mx == 0) break;
-        // the lowest index among the lanes that hold it: mostly one lane, no second reduction
-        const uint32_t holders = __ballot_sync(kFull, best == mx);
-        uint32_t cand = 0xFFFFFFFFu;
-        if (best == mx) {
 #pragma unroll
-            for (int i = VPL - 1; i >= 0; i--)
-                if (key[i] == mx) cand = (uint32_t)(32 * i + lane);
-        }
-        const uint32_t e = (holders & (holders - 1)) == 0 ? __shfl_sync(kFull, cand, __ffs(holders) - 1)
-                                                          : __reduce_min_sync(kFull, cand);
-        if (cand == e) {   // this lane held it
-            best = 0;
+        for (int i = VPL - 1; i >= 0; i--)
+            if (key[i] == mx) cand = (uint32_t)(32 * i + lane);
+        const uint32_t e = __reduce_min_sync(kFull, cand);
 #pragma unroll
-            for (int i = 0; i < VPL; i++) {
-                if ((uint32_t)(32 * i + lane) == e) key[i] = 0;
-                best = best > key[i] ? best : key[i];
-            }
-        }
-        if (lane == j) {
-            id = (int)e;
-            mine = mx;
+        for (int i = 0; i < VPL; i++)
+            if ((uint32_t)(32 * i + lane) == e) key[i] = 0;
+        if (lane == j) mine = make_uint2(e, mx);
+    }
+    return mine;
+}
+
+// One token: lane j < k ends up with choice j (expert id, or -1) and weight.
+// The rounds run on words that join a key's upper 22 bits with the index: one
+// maximum a round, and the word that gave it is unique.  Where two
+// neighbours of the k + 1 largest share those 22 bits and fp32 logits may
+// differ below them (about 1 token in 50), the selection is repeated exactly;
+// the upper 22 bits hold all of a BF16 logit.
+template <int VPL, bool F32>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, const uint32_t (&raw)[VPL], int lane, int& id,
+                                       float& w) {
+    uint32_t word[VPL];
+    uint32_t best = 0;
+    float total = 0.0f, m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; i++) word[i] = bits_key(raw[i]);
+    if (p.score == UW_SCORE_SOFTMAX) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) top = top > word[i] ? top : word[i];
+        top = __reduce_max_sync(kFull, top);
+        m = key_logit(top);   // top = 0 (no choice at all): unused
+        if (!p.renorm && top) {   // the denominator over every logit
+#pragma unroll
+            for (int i = 0; i < VPL; i++)
+                if (word[i]) total += expf(key_logit(word[i]) - m);
+            total = warp_sum(total);
         }
     }
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+        word[i] = word[i] ? (word[i] & 0xFFFFFC00u) | (uint32_t)(1023 - (32 * i + lane)) : 0u;
+        best = best > word[i] ? best : word[i];
+    }
+    uint32_t got = 0;
+    const int rounds = F32 && p.k < 32 ? p.k + 1 : p.k;   // one more: does the last choice stand out
+    for (int j = 0; j < rounds; j++) {
+        const uint32_t mx = __reduce_max_sync(kFull, best);
+        if (mx == 0) break;
+        if (lane == j) got = mx;
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            word[i] = word[i] == mx ? 0u : word[i];
+            best = best > word[i] ? best : word[i];
+        }
+    }
+    id = got && lane < p.k ? 1023 - (int)(got & 1023u) : -1;
+    uint32_t mine = 0;
+    bool close = false;
+    if (F32) {
+        const uint32_t before = __shfl_up_sync(kFull, got, 1);
+        close = lane && got && (before >> 10) == (got >> 10);
+        // k = 32 has no extra round: what is left over is compared with the last choice
+        const uint32_t last = __shfl_sync(kFull, got, 31);
+        if (p.k == 32) close |= best && (best >> 10) == (last >> 10);
+    }
+    if (F32 && __any_sync(kFull, close)) {
+        const uint2 x = select_exact<VPL>(p, t, lane);
+        id = (int)x.x;
+        mine = x.y;
+    } else if (id >= 0) {
+        mine = F32 ? bits_key(__ldg(reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + id)) : got & 0xFFFFFC00u;
+    }
+    if (!F32 && mine) mine |= mine >> 31 ? 0u : 0x3FFu;   // a negative logit's key has its low bits set
     const float x = key_logit(mine);
     float s = 0.0f;
     if (mine) s = p.score == UW_SCORE_SOFTMAX ? expf(x - m) : 1.0f / (1.0f + expf(-x));
@@ -126,22 +183,26 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
 }
 
 // Positions of the CTA's choices, the offsets (CTA 0) and the rows of the
-// slots.  `sm` holds base[E], total[E + 1] and wcount[warps][E].
-__device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
+// slots.  `sm` holds base[E], total[E + 1] and wcount[warps][E].  A single CTA
+// brings its own counts and choices in shared memory, else they are read from
+// what k_route_choose wrote.
+__device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int ctas, const int32_t* counts, const int32_t* ids) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.E;
     int32_t* base = sm;
     int32_t* total = sm + E;
     int32_t* wcount = total + E + 1;
     for (int i = tid; i < 2 * E + 1 + kRankWarps * E; i += kRouteThreads) sm[i] = 0;
     __syncthreads();
-    // counts of the CTAs before this one, and of all: the threads cover E
-    // experts times as many row groups as fit
-    {
+    if (counts) {
+        for (int e = tid; e < E; e += kRouteThreads) total[e] = counts[e];
+    } else {
+        // counts of the CTAs before this one, and of all: the threads cover E
+        // experts times as many row groups as fit
         const int groups = kRouteThreads / E > 1 ? kRouteThreads / E : 1;
         for (int i = tid; i < groups * E; i += kRouteThreads) {
             const int e = i % E, g = i / E;
             int before = 0, all = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int b = g; b < ctas; b += groups) {
                 const int c = __ldcg(p.hist + (int64_t)b * E + e);
                 all += c;
@@ -157,11 +218,11 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
     const int64_t first = t0 * p.k;
     const int64_t n = t1 > t0 ? (t1 - t0) * p.k : 0;
     const int64_t per = ((n + kRankWarps - 1) / kRankWarps + 31) / 32 * 32;
-    const int64_t lo = warp < kRankWarps ? per * warp : n, hi = warp < kRankWarps ? per * (warp + 1) : n;
+    const int64_t lo = per * warp, hi = per * (warp + 1);
     const int64_t w0 = first + (lo < n ? lo : n), w1 = first + (hi < n ? hi : n);
-    int32_t* mine = wcount + (warp < kRankWarps ? warp : 0) * E;
+    int32_t* mine = wcount + warp * E;
     for (int64_t i = w0 + lane; i < w1; i += 32) {
-        const int e = p.ids[i];
+        const int e = ids[i];
         if (e >= 0) atomicAdd(&mine[e], 1);
     }
     __syncthreads();
@@ -185,12 +246,31 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
         if (lane == 31) total[E] = run;
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kRouteThreads) {
-        int at = total[e] + base[e];
-        for (int w = 0; w < kRankWarps; w++) {
-            const int c = wcount[w * E + e];
-            wcount[w * E + e] = at;
-            at += c;
+    // first slot of every warp and expert: the warps' counts of an expert are
+    // scanned by `share` neighbouring lanes, kRankWarps / share rows each
+    {
+        int share = 1;
+        while (share < 32 && 2 * share * E <= kRouteThreads) share *= 2;
+        const int rows = kRankWarps / share;
+        for (int i0 = 0; i0 < E * share; i0 += kRouteThreads) {
+            const int i = i0 + tid, e = i / share, part = i % share;
+            const bool in = e < E;
+            int sum = 0;
+            if (in)
+                for (int w = 0; w < rows; w++) sum += wcount[(part * rows + w) * E + e];
+            int run = sum;
+            for (int d = 1; d < share; d <<= 1) {
+                const int v = __shfl_up_sync(kFull, run, d, share);
+                if (part >= d) run += v;
+            }
+            if (in) {
+                int at = total[e] + base[e] + run - sum;
+                for (int w = 0; w < rows; w++) {
+                    const int c = wcount[(part * rows + w) * E + e];
+                    wcount[(part * rows + w) * E + e] = at;
+                    at += c;
+                }
+            }
         }
     }
     if (blockIdx.x == 0)
@@ -198,7 +278,7 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
     __syncthreads();
     for (int64_t i0 = w0; i0 < w1; i0 += 32) {
         const int64_t i = i0 + lane;
-        const int e = i < w1 ? p.ids[i] : -1;
+        const int e = i < w1 ? ids[i] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         int slot = -1;
         if (e >= 0) slot = mine[e] + __popc(same & ((1u << lane) - 1u));
@@ -219,37 +299,44 @@ __device__ void place(const RouteParams& p, int32_t* sm, int ctas) {
 template <int VPL, bool F32>
 __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParams p) {
     extern __shared__ int32_t sm[];
+    int32_t* counts = sm;
+    int32_t* ids = sm + p.E;   // a single CTA keeps its choices here too
+    const bool single = gridDim.x == 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) counts[e] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) sm[e] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
+    uint32_t raw[VPL], next[VPL];
+    if (t0 + warp < t1) load_logits<VPL, F32>(p, t0 + warp, lane, next);
     for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++) raw[i] = next[i];
+        if (t + kRouteWarps < t1) load_logits<VPL, F32>(p, t + kRouteWarps, lane, next);   // the next token's, meanwhile
         int id;
         float w;
-        choose<VPL, F32>(p, t, lane, id, w);
+        choose<VPL, F32>(p, t, raw, lane, id, w);
         if (lane < p.k) {
             p.ids[t * p.k + lane] = id;
             p.weights[t * p.k + lane] = w;
-            if (id >= 0) atomicAdd(&sm[id], 1);
+            if (id >= 0) atomicAdd(&counts[id], 1);
+            if (single) ids[t * p.k + lane] = id;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = sm[e];
-    if (gridDim.x == 1) {   // a single CTA places its choices at once
-        __threadfence();
-        __syncthreads();
-        place(p, sm, 1);
-    }
+    if (single)
+        place(p, ids + kSingle, 1, counts, ids);
+    else
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = counts[e];
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams p) {
     extern __shared__ int32_t sm[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    place(p, sm, (int)gridDim.x);
+    place(p, sm, (int)gridDim.x, nullptr, p.ids);
 }
 
 template <typename P>
@@ -406,7 +493,7 @@ __global__ void __launch_bounds__(kCombineThreads, IN32 ? 2 : 4) k_combine(const
 // CTAs of the router: one up to 512 choices (a single launch), else up to one
 // per SM, 8 tokens at least in each.
 int route_blocks(int64_t T, int k) {
-    if (T * k <= 512) return 1;
+    if (T * k <= kSingle) return 1;
     const int64_t b = (T + 7) / 8;
     return (int)(b < num_sms() ? b : num_sms());
 }
@@ -432,7 +519,7 @@ cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k
     p.hist = hist;
     const size_t smem = (size_t)(2 * E + 1 + kRankWarps * E) * 4;
     const RouteKernel choose_k = in_f32 ? route_kernel<true>(E) : route_kernel<false>(E);
-    const size_t smem_c = ctas == 1 ? smem : (size_t)E * 4;
+    const size_t smem_c = (size_t)E * 4 + (ctas == 1 ? kSingle * 4 + smem : 0);
     cudaError_t e = smem_c > 48 * 1024 ? set_smem_attr((const void*)choose_k, (int)smem_c) : cudaSuccess;
     if (e == cudaSuccess && smem > 48 * 1024) e = set_smem_attr((const void*)k_route_place, (int)smem);
     if (e != cudaSuccess) return e;

@@ -450,7 +450,7 @@ uw_status uw_mx_gemm(const uint16_t* X, const uw_mx_matrix* X_mx, int64_t M, con
  *   rows[T * k]: the token of each slot, -1 from slot offsets[E] on.
  *   pos[T, k]: the slot of each choice, -1: no choice.
  * 1 <= k <= 32, k <= E <= 1024, T * k < 2^31.  T = 0 writes offsets only.
- * workspace: 256-byte aligned, any contents. */
+ * workspace: 256-byte aligned, any contents (NULL where its size is 0). */
 enum { UW_SCORE_SOFTMAX = 0, UW_SCORE_SIGMOID = 1 };
 
 uw_status uw_route_workspace(int64_t T, int E, int k, size_t* bytes);

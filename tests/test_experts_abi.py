@@ -92,8 +92,8 @@ def test_route_refusals(L):
     for T, E, k, want in ((-1, 8, 2, 1), (4, 0, 1, 1), (4, 8, 0, 1), (4, 8, 9, 2), (4, 1025, 2, 2), (4, 64, 33, 2), (1 << 30, 8, 2, 2)):
         assert L.uw_route_workspace(T, E, k, ctypes.byref(n)) == want, (T, E, k)
         assert L.uw_route(A, 1, T, E, k, 0, 0, 1.0, A, A, A, A, A, A, 1 << 30, None) == want
-    assert L.uw_route_workspace(100, 8, 2, ctypes.byref(n)) == 0 and n.value > 0
-    args = [A, 1, 100, 8, 2, 0, 0, 1.0, A, A, A, A, A, A, 1 << 30, None]
+    assert L.uw_route_workspace(1000, 8, 2, ctypes.byref(n)) == 0 and n.value > 0
+    args = [A, 1, 1000, 8, 2, 0, 0, 1.0, A, A, A, A, A, A, 1 << 30, None]
     for i, v, want in ((0, None, 1), (0, A + 2, 1), (5, 2, 1), (8, None, 1), (9, None, 1), (10, None, 1), (11, None, 1),
                        (12, None, 1), (12, A + 2, 1), (13, None, 5), (13, A + 128, 5), (14, 16, 5)):
         a = list(args)

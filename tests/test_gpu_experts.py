@@ -248,6 +248,21 @@ def test_route_masks_and_extremes(score, renorm):
     assert r.ids[12].tolist() == list(range(k))
 
 
+@pytest.mark.parametrize("E,k", [(40, 8), (64, 32), (32, 32), (300, 5)])
+def test_route_logits_that_differ_in_their_last_bits(E, k):
+    """Neighbours a few units in the last place apart, equal ones among them, also at the border of the choice."""
+    bits = torch.randint(0, 40, (257, E), generator=_gen(E), device="cuda").int()
+    x = (torch.full((257, E), 1.5, device="cuda").view(torch.int32) + bits).view(torch.float32)
+    x[::2] = -x[::2]
+    _check_route(x, k, "softmax", True)
+    y = torch.randn(257, E, generator=_gen(1), device="cuda")
+    order = y.sort(dim=1, descending=True).values
+    if k < E:
+        edge = order[:, k - 1:k]
+        y = torch.where(y == order[:, k:k + 1], (edge.view(torch.int32) - 1).view(torch.float32), y)   # beside the last choice
+    _check_route(y, k, "sigmoid", False)
+
+
 def test_route_empty_and_all_masked():
     r = uw.uw_route(torch.empty(0, 8, device="cuda"), 2)
     assert r.offsets.tolist() == [0] * 9 and r.ids.shape == (0, 2) and r.rows.shape == (0,)
