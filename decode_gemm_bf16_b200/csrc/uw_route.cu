@@ -27,9 +27,7 @@ int route_status_take() { return unit_status_take(); }
 
 namespace {
 
-constexpr int kRouteThreads = 1024;
-constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRankWarps = kRouteWarps;   // warps that rank choices (a row of counts each)
+constexpr int kRouteThreads = 1024;   // at most; a single CTA takes a warp per token
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kSingle = 512;     // choices up to which one CTA does everything
 
@@ -76,11 +74,12 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
 
 // Order-preserving key of a logit's bits; 0: never chosen (NaN, -infinity).
 // +infinity counts as the largest finite number, -0 as 0.
-__device__ __forceinline__ uint32_t bits_key(uint32_t b) {
-    if (b == 0x7F800000u) b = 0x7F7FFFFFu;
-    if (b == 0x80000000u) b = 0;
-    const bool out = (b & 0x7FFFFFFFu) > 0x7F800000u || b == 0xFF800000u;
-    return out ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+__device__ __forceinline__ uint32_t bits_key(uint32_t bits) {
+    const uint32_t b = __float_as_uint(__uint_as_float(bits) + 0.0f);   // -0 -> 0, every NaN -> a positive one
+    const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    const uint32_t top = 0xFF7FFFFFu;                                    // the largest finite number's
+    // -infinity: 0x007FFFFF; numbers from 0x00800000; infinity: 0xFF800000; NaN above
+    return k - 0x00800000u > 0xFF800000u - 0x00800000u ? 0u : k < top ? k : top;
 }
 
 // The k largest keys in falling order, equal keys by index: lane j < k ends up
@@ -149,12 +148,12 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, const ui
         const uint32_t mx = __reduce_max_sync(kFull, best);
         if (mx == 0) break;
         if (lane == j) got = mx;
-        best = 0;
+        // the largest word below mx: word - mx wraps to the top of the range below it, to its bottom from it up
+        uint32_t below = 0;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            word[i] = word[i] == mx ? 0u : word[i];
-            best = best > word[i] ? best : word[i];
-        }
+        for (int i = 0; i < VPL; i++) below = __viaddmax_u32(word[i], 0u - mx, below);
+        best = below + mx;
+        best = best < mx ? best : 0u;
     }
     id = got && lane < p.k ? 1023 - (int)(got & 1023u) : -1;
     uint32_t mine = 0;
@@ -187,20 +186,33 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, const ui
 // brings its own counts and choices in shared memory, else they are read from
 // what k_route_choose wrote.
 __device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int ctas, const int32_t* counts, const int32_t* ids) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.E;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.E, threads = blockDim.x, warps = threads >> 5;
     int32_t* base = sm;
     int32_t* total = sm + E;
     int32_t* wcount = total + E + 1;
-    for (int i = tid; i < 2 * E + 1 + kRankWarps * E; i += kRouteThreads) sm[i] = 0;
+    for (int i = tid; i < 2 * E + 1 + warps * E; i += threads) sm[i] = 0;
+    // a warp owns a contiguous run of the CTA's entries; its first 32 are read once
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
+    const int64_t first = t0 * p.k;
+    const int64_t n = t1 > t0 ? (t1 - t0) * p.k : 0;
+    const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t lo = per * warp, hi = per * (warp + 1);
+    const int64_t w0 = first + (lo < n ? lo : n), w1 = first + (hi < n ? hi : n);
+    if (!counts) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    const int e0 = w0 + lane < w1 ? ids[w0 + lane] : -1;
     __syncthreads();
     if (counts) {
-        for (int e = tid; e < E; e += kRouteThreads) total[e] = counts[e];
+        for (int e = tid; e < E; e += threads) total[e] = counts[e];
     } else {
         // counts of the CTAs before this one, and of all: the threads cover E
         // experts times as many row groups as fit
-        const int groups = kRouteThreads / E > 1 ? kRouteThreads / E : 1;
-        for (int i = tid; i < groups * E; i += kRouteThreads) {
-            const int e = i % E, g = i / E;
+        const int groups = threads / E > 1 ? threads / E : 1;
+        if (tid < groups * E) {   // E <= threads
+            const int e = tid % E, g = tid / E;
             int before = 0, all = 0;
 #pragma unroll 16
             for (int b = g; b < ctas; b += groups) {
@@ -212,16 +224,9 @@ __device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int cta
             if (all) atomicAdd(&total[e], all);
         }
     }
-    // this CTA's choices per warp: warp w owns a contiguous run of its entries
-    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
-    const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
-    const int64_t first = t0 * p.k;
-    const int64_t n = t1 > t0 ? (t1 - t0) * p.k : 0;
-    const int64_t per = ((n + kRankWarps - 1) / kRankWarps + 31) / 32 * 32;
-    const int64_t lo = per * warp, hi = per * (warp + 1);
-    const int64_t w0 = first + (lo < n ? lo : n), w1 = first + (hi < n ? hi : n);
     int32_t* mine = wcount + warp * E;
-    for (int64_t i = w0 + lane; i < w1; i += 32) {
+    if (e0 >= 0) atomicAdd(&mine[e0], 1);
+    for (int64_t i = w0 + 32 + lane; i < w1; i += 32) {
         const int e = ids[i];
         if (e >= 0) atomicAdd(&mine[e], 1);
     }
@@ -250,35 +255,32 @@ __device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int cta
     // scanned by `share` neighbouring lanes, kRankWarps / share rows each
     {
         int share = 1;
-        while (share < 32 && 2 * share * E <= kRouteThreads) share *= 2;
-        const int rows = kRankWarps / share;
-        for (int i0 = 0; i0 < E * share; i0 += kRouteThreads) {
-            const int i = i0 + tid, e = i / share, part = i % share;
-            const bool in = e < E;
+        while (2 * share <= warps && 2 * share * E <= threads) share *= 2;
+        const int rows = (warps + share - 1) / share;
+        for (int i0 = 0; i0 < E * share; i0 += threads) {   // one round but for a small single CTA
+            const int i = i0 + tid, e = i / share, part = i % share, r0 = part * rows;
+            const int r1 = e >= E ? r0 : r0 + rows < warps ? r0 + rows : warps;
             int sum = 0;
-            if (in)
-                for (int w = 0; w < rows; w++) sum += wcount[(part * rows + w) * E + e];
+            for (int w = r0; w < r1; w++) sum += wcount[w * E + e];
             int run = sum;
             for (int d = 1; d < share; d <<= 1) {
                 const int v = __shfl_up_sync(kFull, run, d, share);
                 if (part >= d) run += v;
             }
-            if (in) {
-                int at = total[e] + base[e] + run - sum;
-                for (int w = 0; w < rows; w++) {
-                    const int c = wcount[(part * rows + w) * E + e];
-                    wcount[(part * rows + w) * E + e] = at;
-                    at += c;
-                }
+            int at = e < E ? total[e] + base[e] + run - sum : 0;
+            for (int w = r0; w < r1; w++) {
+                const int c = wcount[w * E + e];
+                wcount[w * E + e] = at;
+                at += c;
             }
         }
     }
     if (blockIdx.x == 0)
-        for (int e = tid; e <= E; e += kRouteThreads) p.offsets[e] = total[e];
+        for (int e = tid; e <= E; e += threads) p.offsets[e] = total[e];
     __syncthreads();
     for (int64_t i0 = w0; i0 < w1; i0 += 32) {
         const int64_t i = i0 + lane;
-        const int e = i < w1 ? ids[i] : -1;
+        const int e = i0 == w0 ? e0 : i < w1 ? ids[i] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         int slot = -1;
         if (e >= 0) slot = mine[e] + __popc(same & ((1u << lane) - 1u));
@@ -287,12 +289,12 @@ __device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int cta
         __syncwarp();
         if (i < w1) {
             p.pos[i] = slot;
-            if (slot >= 0) p.rows[slot] = (int32_t)(i / p.k);
+            if (slot >= 0) p.rows[slot] = (int32_t)((uint32_t)i / (uint32_t)p.k);   // T k < 2^31
         }
     }
     // slots that no choice fills
     const int64_t all = p.T * p.k;
-    for (int64_t i = total[E] + (int64_t)blockIdx.x * kRouteThreads + tid; i < all; i += (int64_t)ctas * kRouteThreads)
+    for (int64_t i = total[E] + (int64_t)blockIdx.x * threads + tid; i < all; i += (int64_t)ctas * threads)
         p.rows[i] = -1;
 }
 
@@ -302,8 +304,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParam
     int32_t* counts = sm;
     int32_t* ids = sm + p.E;   // a single CTA keeps its choices here too
     const bool single = gridDim.x == 1;
+    const int threads = blockDim.x, warps = threads >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) counts[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += threads) counts[e] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
@@ -311,10 +314,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParam
     const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
     uint32_t raw[VPL], next[VPL];
     if (t0 + warp < t1) load_logits<VPL, F32>(p, t0 + warp, lane, next);
-    for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
+    for (int64_t t = t0 + warp; t < t1; t += warps) {
 #pragma unroll
         for (int i = 0; i < VPL; i++) raw[i] = next[i];
-        if (t + kRouteWarps < t1) load_logits<VPL, F32>(p, t + kRouteWarps, lane, next);   // the next token's, meanwhile
+        if (t + warps < t1) load_logits<VPL, F32>(p, t + warps, lane, next);   // the next token's, meanwhile
         int id;
         float w;
         choose<VPL, F32>(p, t, raw, lane, id, w);
@@ -329,13 +332,11 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParam
     if (single)
         place(p, ids + kSingle, 1, counts, ids);
     else
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = counts[e];
+        for (int e = threadIdx.x; e < p.E; e += threads) p.hist[(int64_t)blockIdx.x * p.E + e] = counts[e];
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_route_place(const RouteParams p) {
     extern __shared__ int32_t sm[];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     place(p, sm, (int)gridDim.x, nullptr, p.ids);
 }
 
@@ -517,13 +518,19 @@ cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k
     p.rows = rows;
     p.pos = pos;
     p.hist = hist;
-    const size_t smem = (size_t)(2 * E + 1 + kRankWarps * E) * 4;
+    // a single CTA: a warp per token, 4 at least
+    int threads = kRouteThreads;
+    if (ctas == 1) {
+        const int64_t want = 32 * (T > 4 ? T : 4);
+        threads = (int)(want < kRouteThreads ? want : kRouteThreads);
+    }
+    const size_t smem = (size_t)(2 * E + 1 + threads / 32 * E) * 4;
     const RouteKernel choose_k = in_f32 ? route_kernel<true>(E) : route_kernel<false>(E);
     const size_t smem_c = (size_t)E * 4 + (ctas == 1 ? kSingle * 4 + smem : 0);
     cudaError_t e = smem_c > 48 * 1024 ? set_smem_attr((const void*)choose_k, (int)smem_c) : cudaSuccess;
     if (e == cudaSuccess && smem > 48 * 1024) e = set_smem_attr((const void*)k_route_place, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(choose_k, ctas, kRouteThreads, smem_c, s, p);
+    e = launch_pdl(choose_k, ctas, threads, smem_c, s, p);
     if (e != cudaSuccess || ctas == 1) return e;
     return launch_pdl<RouteParams>(k_route_place, ctas, kRouteThreads, smem, s, p);
 }
