@@ -11,8 +11,8 @@ The method: "CloudflareæŽ¨å‡ºUnweightç„¡æå£“ç¸®ç³»çµ±ï¼Œå°‡LLMæ¨¡åž‹å¤§å°å£“ç
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -531,22 +531,25 @@ def uw_plan_load_json(path: str, cap: int = 4096) -> list:
 # device that holds them whatever the current device is, and allocate outputs
 # and workspaces from torch's caching allocator on the stream they use, so that
 # calls on several streams and captured graphs never share a workspace unless
-# the caller passes one.
-_EMPTY_CTX = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    """(context, stream handle): `device` current, and `stream` (default: the
-    device's current stream) current on it so that allocations belong to it."""
+# the caller passes one.  Decoding calls take a few microseconds on the device,
+# so the way to the library is kept short: one query of the current stream, no
+# context manager unless another device or stream is asked for, sizes that
+# depend on shapes alone looked up once.
+def _run(device: torch.device, stream, fn, *args):
+    """fn(stream handle, *args) with `device` current and `stream` (default:
+    the device's current stream) current on it, so that allocations belong to it."""
+    index = device.index
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-        ctx = _EMPTY_CTX if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        return ctx, handle
+        if torch._C._cuda_getDevice() == index:
+            return fn(torch._C._cuda_getCurrentRawStream(index), *args)
+        with torch.cuda.device(device):
+            return fn(torch._C._cuda_getCurrentRawStream(index), *args)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    with torch.cuda.stream(stream):
+        return fn(stream.cuda_stream, *args)
 
 
 def _need(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True) -> torch.Tensor:
@@ -554,9 +557,9 @@ def _need(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True
         raise ValueError(f"{name}: expected a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
@@ -564,26 +567,34 @@ def _need(t, name: str, dtypes, shape=None, device=None, contiguous: bool = True
 
 
 _BF16, _FLOAT, _I32, _U8 = (torch.bfloat16,), (torch.bfloat16, torch.float32), (torch.int32,), (torch.uint8,)
+_F32 = (torch.float32,)
 
 
-def _input(t, name: str, dtypes, device=None) -> torch.Tensor:
-    """An input matrix: any strides (copied to rows of consecutive values when
-    it is not laid out so)."""
-    t = _need(t, name, dtypes, device=device, contiguous=False)
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """An input matrix of any strides as 16-byte aligned rows of consecutive
+    values (copied where it is not laid out so)."""
     return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
-def _output(out, shape, out_f32: bool, device) -> torch.Tensor:
+def _output(out, shape, out_f32: bool, like: torch.Tensor) -> torch.Tensor:
     dtype = torch.float32 if out_f32 else torch.bfloat16
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _need(out, "out", (dtype,), shape, device)
+        return like.new_empty(shape, dtype=dtype)
+    return _need(out, "out", (dtype,), shape, like.device)
 
 
-def _scratch(ws, nbytes: int, device) -> torch.Tensor:
+def _scratch(ws, nbytes: int, device: torch.device) -> torch.Tensor:
     if ws is None:
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     return _need(ws, "ws", _U8, device=device)
+
+
+@functools.lru_cache(maxsize=4096)
+def uw_mx_bytes(batch: int, rows: int, K: int) -> tuple:
+    """(code bytes, scale bytes) of `batch` matrices [rows, K]."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().uw_mx_bytes(int(batch), int(rows), int(K), ctypes.byref(c), ctypes.byref(s)), "uw_mx_bytes")
+    return c.value, s.value
 
 
 class MxMatrix:
@@ -596,61 +607,55 @@ class MxMatrix:
         if codes.dim() not in (2, 3):
             raise ValueError(f"codes: expected [rows, K/2] or [batch, rows, K/2], got {tuple(codes.shape)}")
         _need(scales, "scales", _U8, device=codes.device)
-        self.codes, self.scales = codes, scales
-        self.batch = codes.shape[0] if codes.dim() == 3 else 1
-        self.rows, self.K = codes.shape[-2], 2 * codes.shape[-1]
+        self._hold(codes, scales, tuple(codes.shape[:-1]) + (2 * codes.shape[-1],))
         nb = uw_mx_bytes(self.batch, self.rows, self.K)[1]
         if scales.numel() != nb:
             raise ValueError(f"scales: expected {nb} bytes, got {scales.numel()}")
+
+    def _hold(self, codes, scales, shape):
+        self.codes, self.scales, self.shape, self.device = codes, scales, shape, codes.device
+        self.batch = shape[0] if len(shape) == 3 else 1
+        self.rows, self.K = shape[-2:]
         self._desc = MxDesc(codes.data_ptr(), scales.data_ptr(), self.batch, self.rows, self.K)
-
-    @property
-    def shape(self):
-        return (*self.codes.shape[:-1], self.K)
-
-    @property
-    def device(self):
-        return self.codes.device
 
     @property
     def nbytes(self) -> int:
         return self.codes.numel() + self.scales.numel()
 
 
-def uw_mx_bytes(batch: int, rows: int, K: int) -> tuple:
-    """(code bytes, scale bytes) of `batch` matrices [rows, K]."""
-    c, s = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().uw_mx_bytes(int(batch), int(rows), int(K), ctypes.byref(c), ctypes.byref(s)), "uw_mx_bytes")
-    return c.value, s.value
-
-
 def uw_mx_quantize(X: torch.Tensor, out: Optional[MxMatrix] = None, stream=None) -> MxMatrix:
     """X[rows, K] or [batch, rows, K] (BF16 or float32) to the microscaled 4-bit form."""
-    if isinstance(X, torch.Tensor) and X.dim() not in (2, 3):
+    _need(X, "X", _FLOAT, contiguous=False)
+    if X.dim() not in (2, 3):
         raise ValueError(f"X: expected [rows, K] or [batch, rows, K], got {tuple(X.shape)}")
-    device = _need(X, "X", _FLOAT, contiguous=False).device
-    ctx, handle = _on(device, stream)
-    with ctx:
-        X = _input(X, "X", _FLOAT)
-        batch = X.shape[0] if X.dim() == 3 else 1
-        rows, K = X.shape[-2:]
-        if out is None:
-            nb = uw_mx_bytes(batch, rows, K)[1]
-            out = MxMatrix(torch.empty(*X.shape[:-1], K // 2, dtype=torch.uint8, device=device),
-                           torch.empty(nb, dtype=torch.uint8, device=device))
-        elif out.shape != tuple(X.shape) or out.device != device:
-            raise ValueError(f"out: expected {tuple(X.shape)} on {device}, got {out.shape} on {out.device}")
-        _check(lib().uw_mx_quantize(X.data_ptr(), 1 if X.dtype == torch.float32 else 0, batch, rows, K, out.codes.data_ptr(),
-                                    out.scales.data_ptr(), handle), "uw_mx_quantize")
+    return _run(X.device, stream, _mx_quantize, X, out)
+
+
+def _mx_quantize(handle, X, out):
+    X = _rows(X)
+    shape = tuple(X.shape)
+    batch = shape[0] if len(shape) == 3 else 1
+    rows, K = shape[-2:]
+    if out is None:
+        nb = uw_mx_bytes(batch, rows, K)[1]
+        out = MxMatrix.__new__(MxMatrix)
+        out._hold(X.new_empty(shape[:-1] + (K // 2,), dtype=torch.uint8), X.new_empty(nb, dtype=torch.uint8), shape)
+    elif out.shape != shape or out.device != X.device:
+        raise ValueError(f"out: expected {shape} on {X.device}, got {out.shape} on {out.device}")
+    d = out._desc
+    _check(lib().uw_mx_quantize(X.data_ptr(), 1 if X.dtype == torch.float32 else 0, batch, rows, K, d.codes, d.scales, handle),
+           "uw_mx_quantize")
     return out
 
 
 def uw_mx_dequantize(m: MxMatrix, out: Optional[torch.Tensor] = None, out_f32: bool = False, stream=None) -> torch.Tensor:
     """The values of a microscaled matrix, exactly."""
-    ctx, handle = _on(m.device, stream)
-    with ctx:
-        out = _output(out, m.shape, out_f32, m.device)
-        _check(lib().uw_mx_dequantize(ctypes.byref(m._desc), out.data_ptr(), 1 if out_f32 else 0, handle), "uw_mx_dequantize")
+    return _run(m.device, stream, _mx_dequantize, m, out, out_f32)
+
+
+def _mx_dequantize(handle, m, out, out_f32):
+    out = _output(out, m.shape, out_f32, m.codes)
+    _check(lib().uw_mx_dequantize(ctypes.byref(m._desc), out.data_ptr(), 1 if out_f32 else 0, handle), "uw_mx_dequantize")
     return out
 
 
@@ -660,26 +665,33 @@ def uw_mx_gemm_workspace(M: int, N: int, K: int, x_mx: bool = False) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx_gemm_bytes(index: int, M: int, N: int, K: int, x_mx: bool) -> int:   # index: sizes follow the device's SM count
+    return uw_mx_gemm_workspace(M, N, K, x_mx)
+
+
 def uw_mx_gemm(X, W: MxMatrix, out: Optional[torch.Tensor] = None, out_f32: bool = False, ws: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """Y[M, N] = X . W^T with W in the microscaled 4-bit form.  X: BF16 [M, K]
-    (the weights are rebuilt to BF16 on chip) or an MxMatrix (4-bit products)."""
-    device = W.device
+    (see the header for how its values enter) or an MxMatrix (4-bit products)."""
     mx = isinstance(X, MxMatrix)
-    if mx and X.device != device:
-        raise ValueError(f"X: on {X.device}, expected {device}")
-    ctx, handle = _on(device, stream)
-    with ctx:
-        if not mx:
-            X = _input(X, "X", _BF16, device)
-        if len(X.shape) != 2 or X.shape[1] != W.K:
-            raise ValueError(f"X: expected [M, {W.K}], got {tuple(X.shape)}")
-        M = X.shape[0]
-        need = uw_mx_gemm_workspace(M, W.rows, W.K, mx)
-        out = _output(out, (M, W.rows), out_f32, device)
-        ws = _scratch(ws, need, device)
-        _check(lib().uw_mx_gemm(None if mx else X.data_ptr(), ctypes.byref(X._desc) if mx else None, M, ctypes.byref(W._desc),
-                                out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel(), handle), "uw_mx_gemm")
+    if not mx:
+        _need(X, "X", _BF16, device=W.device, contiguous=False)
+    elif X.device != W.device:
+        raise ValueError(f"X: on {X.device}, expected {W.device}")
+    if len(X.shape) != 2 or X.shape[1] != W.K:
+        raise ValueError(f"X: expected [M, {W.K}], got {tuple(X.shape)}")
+    return _run(W.device, stream, _mx_gemm, X, W, mx, out, out_f32, ws)
+
+
+def _mx_gemm(handle, X, W, mx, out, out_f32, ws):
+    M, N = X.shape[0], W.rows
+    if not mx:
+        X = _rows(X)
+    out = _output(out, (M, N), out_f32, W.codes)
+    ws = _scratch(ws, _mx_gemm_bytes(W.device.index, M, N, W.K, mx), W.device)
+    _check(lib().uw_mx_gemm(None if mx else X.data_ptr(), ctypes.byref(X._desc) if mx else None, M, ctypes.byref(W._desc),
+                            out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel(), handle), "uw_mx_gemm")
     return out
 
 
@@ -698,43 +710,39 @@ def uw_route_workspace(T: int, E: int, k: int) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _route_bytes(index: int, T: int, E: int, k: int) -> int:
+    return uw_route_workspace(T, E, k)
+
+
 def uw_route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = False, scale: float = 1.0,
              ws: Optional[torch.Tensor] = None, stream=None) -> Route:
     """The k experts of every token of logits[T, E] (BF16 or float32), their
     weights, and the slots sorted by expert."""
     if score not in SCORES:
         raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
-    device = _need(logits, "logits", _FLOAT, contiguous=False).device
+    _need(logits, "logits", _FLOAT, contiguous=False)
     if logits.dim() != 2:
         raise ValueError(f"logits: expected [T, E], got {tuple(logits.shape)}")
-    ctx, handle = _on(device, stream)
-    with ctx:
+    return _run(logits.device, stream, _route, logits, int(k), SCORES[score], renorm, scale, ws)
+
+
+def _route(handle, logits, k, score, renorm, scale, ws):
+    if not logits.is_contiguous():
         logits = logits.contiguous()
-        T, E = logits.shape
-        need = uw_route_workspace(T, E, k)
-        i32 = dict(dtype=torch.int32, device=device)
-        r = Route(torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device=device), torch.empty(E + 1, **i32),
-                  torch.empty(T * k, **i32), torch.empty(T, k, **i32))
-        if ws is not None or need:
-            ws = _scratch(ws, need, device)
-        _check(lib().uw_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, T, E, int(k), SCORES[score],
-                              1 if renorm else 0, float(scale), r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
-                              r.rows.data_ptr(), r.pos.data_ptr(), ws.data_ptr() if ws is not None else None,
-                              ws.numel() if ws is not None else 0, handle), "uw_route")
-    return r
-
-
-def _group_args(slots: int, E: int, N: int, K: int, W, up) -> GroupArgs:
-    a = GroupArgs()
-    a.slots, a.E, a.N, a.K = slots, E, N, K
-    if isinstance(W, MxMatrix):
-        a.W_mx = ctypes.pointer(W._desc)
-        if up is not None:
-            a.up_mx = ctypes.pointer(up._desc)
-    else:
-        a.W = W.data_ptr()
-        a.up = up.data_ptr() if up is not None else None
-    return a
+    T, E = logits.shape
+    need = _route_bytes(logits.get_device(), T, E, k)
+    i32 = torch.int32
+    ids = logits.new_empty((T, k), dtype=i32)
+    pos = torch.empty_like(ids)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    offsets, rows = logits.new_empty(E + 1, dtype=i32), logits.new_empty(T * k, dtype=i32)
+    if ws is not None or need:
+        ws = _scratch(ws, need, logits.device)
+    _check(lib().uw_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, T, E, k, score, 1 if renorm else 0, scale,
+                          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), handle), "uw_route")
+    return Route(ids, weights, offsets, rows, pos)
 
 
 def _expert_weight(W, name: str):
@@ -747,14 +755,25 @@ def _expert_weight(W, name: str):
     return tuple(W.shape)
 
 
-def uw_gemm_grouped_workspace(slots: int, W, up=None, gathered: bool = False) -> int:
-    """Workspace bytes of uw_gemm_grouped (gathered: with `rows`)."""
-    E, N, K = _expert_weight(W, "W")
-    a = _group_args(slots, E, N, K, W, up)
-    a.rows = 4 if gathered else None   # read as given or not
+def _group_args(X, x_rows, rows, slots, offsets, E, N, K, W, up, out, out_f32) -> GroupArgs:
+    if isinstance(W, MxMatrix):
+        return GroupArgs(X, x_rows, rows, slots, offsets, E, N, K, None, None, ctypes.pointer(W._desc),
+                         ctypes.pointer(up._desc) if up is not None else None, out, out_f32)
+    return GroupArgs(X, x_rows, rows, slots, offsets, E, N, K, W.data_ptr(), up.data_ptr() if up is not None else None, None,
+                     None, out, out_f32)
+
+
+def _group_bytes(a: GroupArgs) -> int:
     n = ctypes.c_size_t()
     _check(lib().uw_gemm_grouped_workspace(ctypes.byref(a), ctypes.byref(n)), "uw_gemm_grouped_workspace")
     return n.value
+
+
+def uw_gemm_grouped_workspace(slots: int, W, up=None, gathered: bool = False) -> int:
+    """Workspace bytes of uw_gemm_grouped (gathered: with `rows`)."""
+    E, N, K = _expert_weight(W, "W")
+    # `rows` is read as given or not
+    return _group_bytes(_group_args(None, 0, 4 if gathered else None, int(slots), None, E, N, K, W, up, None, 0))
 
 
 def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, up=None,
@@ -765,51 +784,56 @@ def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[to
     W, up: BF16 [E, N, K] or MxMatrix with a batch of E.  rows: the row of X of
     each slot (default: slot s reads row s).  Rows of the output outside the
     offsets are left as they were."""
-    E, N, K = _expert_weight(W, "W")
+    shape = _expert_weight(W, "W")
     device = W.device
     if up is not None:
         if isinstance(up, MxMatrix) != isinstance(W, MxMatrix):
             raise ValueError("W and up: expected weights of one kind")
-        if _expert_weight(up, "up") != (E, N, K) or up.device != device:
-            raise ValueError(f"up: expected {(E, N, K)} on {device}")
-    _need(offsets, "offsets", _I32, (E + 1,), device)
+        if _expert_weight(up, "up") != shape or up.device != device:
+            raise ValueError(f"up: expected {shape} on {device}, got {tuple(up.shape)} on {up.device}")
+    _need(offsets, "offsets", _I32, (shape[0] + 1,), device)
     if rows is not None:
         _need(rows, "rows", _I32, device=device)
         if rows.dim() != 1:
             raise ValueError(f"rows: expected [slots], got {tuple(rows.shape)}")
-    ctx, handle = _on(device, stream)
-    with ctx:
-        X = _input(X, "X", _BF16, device)
-        if X.dim() != 2 or X.shape[1] != K:
-            raise ValueError(f"X: expected [rows, {K}], got {tuple(X.shape)}")
-        slots = X.shape[0] if rows is None else rows.shape[0]
-        a = _group_args(slots, E, N, K, W, up)
-        a.rows = rows.data_ptr() if rows is not None else None
-        n = ctypes.c_size_t()
-        _check(lib().uw_gemm_grouped_workspace(ctypes.byref(a), ctypes.byref(n)), "uw_gemm_grouped_workspace")
-        out = _output(out, (slots, N), out_f32, device)
-        ws = _scratch(ws, n.value, device)
-        a.X, a.x_rows, a.offsets = X.data_ptr(), X.shape[0], offsets.data_ptr()
-        a.Y, a.out_f32, a.workspace, a.workspace_bytes = out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel()
-        _check(lib().uw_gemm_grouped(ctypes.byref(a), handle), "uw_gemm_grouped")
+    _need(X, "X", _BF16, device=device, contiguous=False)
+    if X.dim() != 2 or X.shape[1] != shape[2]:
+        raise ValueError(f"X: expected [rows, {shape[2]}], got {tuple(X.shape)}")
+    return _run(device, stream, _gemm_grouped, X, W, offsets, rows, up, shape, out, out_f32, ws)
+
+
+def _gemm_grouped(handle, X, W, offsets, rows, up, shape, out, out_f32, ws):
+    X = _rows(X)
+    E, N, K = shape
+    slots = X.shape[0] if rows is None else rows.shape[0]
+    out = _output(out, (slots, N), out_f32, X)
+    a = _group_args(X.data_ptr(), X.shape[0], None if rows is None else rows.data_ptr(), slots, offsets.data_ptr(), E, N, K, W, up,
+                    out.data_ptr(), 1 if out_f32 else 0)
+    ws = _scratch(ws, _group_bytes(a), X.device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _check(lib().uw_gemm_grouped(ctypes.byref(a), handle), "uw_gemm_grouped")
     return out
 
 
 def uw_combine(Z: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, out: Optional[torch.Tensor] = None,
                out_f32: bool = False, stream=None) -> torch.Tensor:
     """Y[t] = sum_j weights[t, j] * Z[pos[t, j]] over the choices with pos >= 0."""
-    device = _need(Z, "Z", _FLOAT, contiguous=False).device
+    _need(Z, "Z", _FLOAT, contiguous=False)
     if Z.dim() != 2:
         raise ValueError(f"Z: expected [slots, N], got {tuple(Z.shape)}")
+    device = Z.device
     _need(pos, "pos", _I32, device=device)
     if pos.dim() != 2:
         raise ValueError(f"pos: expected [T, k], got {tuple(pos.shape)}")
-    _need(weights, "weights", (torch.float32,), pos.shape, device)
-    ctx, handle = _on(device, stream)
-    with ctx:
-        Z = _input(Z, "Z", _FLOAT)
-        T, k = pos.shape
-        out = _output(out, (T, Z.shape[1]), out_f32, device)
-        _check(lib().uw_combine(Z.data_ptr(), 1 if Z.dtype == torch.float32 else 0, Z.shape[0], pos.data_ptr(),
-                                weights.data_ptr(), T, k, Z.shape[1], out.data_ptr(), 1 if out_f32 else 0, handle), "uw_combine")
+    _need(weights, "weights", _F32, pos.shape, device)
+    return _run(device, stream, _combine, Z, pos, weights, out, out_f32)
+
+
+def _combine(handle, Z, pos, weights, out, out_f32):
+    Z = _rows(Z)
+    T, k = pos.shape
+    slots, N = Z.shape
+    out = _output(out, (T, N), out_f32, Z)
+    _check(lib().uw_combine(Z.data_ptr(), 1 if Z.dtype == torch.float32 else 0, slots, pos.data_ptr(), weights.data_ptr(), T, k, N,
+                            out.data_ptr(), 1 if out_f32 else 0, handle), "uw_combine")
     return out
