@@ -304,42 +304,44 @@ __device__ __forceinline__ int mma_n(int rows) {
     return SRC == kGroupMx8 ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;
 }
 
-// The tile list from the offsets, by one warp: 32 runs of experts, one a lane.
-// Tables in shared memory: cum[E + 1], begin[E], count[E].
+// The tile list from the offsets: tables cum[E + 1], begin[E], count[E] in
+// shared memory.  Every thread of the block calls it (it synchronises twice);
+// all offsets are loaded at once, then 32 runs of experts are summed by warp 0.
 __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int64_t slots, int MG, int n_tiles, int32_t* cum,
-                                           int32_t* begin, int32_t* count, int lane) {
-    const int each = (E + 31) / 32, lo = lane * each < E ? lane * each : E, hi = lo + each < E ? lo + each : E;
-    int sum = 0;
+                                           int32_t* begin, int32_t* count) {
+    const int tid = threadIdx.x, lane = tid & 31;
     bool bad = false;
-    for (int e = lo; e < hi; e++) {
-        int64_t b = 0, n = slots;
+    for (int e = tid; e < E; e += blockDim.x) {
+        int64_t o0 = 0, o1 = slots;
         if (offsets) {
-            const int64_t o0 = offsets[e], o1 = offsets[e + 1];
-            bad |= o0 < 0 || o1 < o0 || o1 > slots;
-            b = o0 < 0 ? 0 : o0 > slots ? slots : o0;
-            n = (o1 > slots ? slots : o1) - b;
-            if (n < 0) n = 0;
+            o0 = offsets[e];
+            o1 = offsets[e + 1];
         }
-        begin[e] = (int)b;
-        count[e] = (int)n;
-        sum += (int)((n + MG - 1) / MG) * n_tiles;
+        const bool wrong = o0 < 0 || o1 < o0 || o1 > slots;
+        bad |= wrong;
+        begin[e] = wrong ? 0 : (int)o0;
+        count[e] = wrong ? 0 : (int)(o1 - o0);
     }
-    int run = sum;
+    const int any = __syncthreads_or(bad);
+    if (any && bad) raise_status(UW_ERR_DEVICE);
+    if (tid < 32) {
+        const int each = (E + 31) / 32, lo = lane * each < E ? lane * each : E, hi = lo + each < E ? lo + each : E;
+        int sum = 0;
+        for (int e = lo; e < hi; e++) sum += any ? 0 : (count[e] + MG - 1) / MG * n_tiles;   // falling or past the slots: no tiles at all
+        int run = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (lane >= d) run += v;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, run, d);
+            if (lane >= d) run += v;
+        }
+        int at = run - sum;
+        for (int e = lo; e < hi; e++) {
+            cum[e] = at;
+            at += any ? 0 : (count[e] + MG - 1) / MG * n_tiles;
+        }
+        if (lane == 31) cum[E] = run;
     }
-    int at = run - sum;
-    for (int e = lo; e < hi; e++) {
-        cum[e] = at;
-        at += (count[e] + MG - 1) / MG * n_tiles;
-    }
-    if (lane == 31) cum[E] = run;
-    if (__any_sync(0xFFFFFFFFu, bad)) {   // offsets that fall or pass the slots: no tiles at all
-        for (int e = lane; e <= E; e += 32) cum[e] = 0;
-        if (bad) raise_status(UW_ERR_DEVICE);
-    }
+    __syncthreads();
 }
 
 // k of a stage.
@@ -428,9 +430,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     // complete already (see k_group_split); what it writes is waited for below.
     if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 0) list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count, lane);
     tc_fence_before();
-    __syncthreads();
+    list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -840,10 +841,11 @@ struct PrepParams {
 };
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepK = 512;   // k of a CTA: 16 a lane
+constexpr int kPrepK = 512;     // k of a CTA: 16 a lane
+constexpr int kPrepRows = 16;   // rows of a CTA: 2 a warp
 
-// Rows of split tiles: CTA (slot tile, 512 k); a warp takes a row at a time,
-// 16 values a lane, two lanes a block of 32.  Row r of a tile of n (rounded up
+// Rows of split tiles: CTA (slot tile, 16 of its rows and 512 k); a warp takes
+// two rows, 16 values of each a lane, two lanes a block of 32.  Row r of a tile of n (rounded up
 // to 8) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
 // swizzled rows; their scale bytes lie in front as tcgen05.cp reads them.
 // Bound by reading the rows and writing as many bytes.
@@ -855,8 +857,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p
     int32_t* begin = cum + p.E + 1;
     int32_t* count = begin + p.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) list_tiles(p.offsets, p.E, p.slots, p.MG, 1, cum, begin, count, lane);
-    __syncthreads();
+    list_tiles(p.offsets, p.E, p.slots, p.MG, 1, cum, begin, count);
     if ((int)blockIdx.x >= cum[p.E]) return;
     int e = 0;
     for (int hi = p.E; hi - e > 1;) {
@@ -867,24 +868,37 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p
     const int64_t s0 = (int64_t)begin[e] + (int64_t)m * p.MG;
     const int nrows = count[e] - m * p.MG < p.MG ? count[e] - m * p.MG : p.MG;
     const int n8 = (nrows + 7) & ~7;
-    const int64_t k = (int64_t)blockIdx.y * kPrepK + 16 * lane;
+    const int segs = (int)((p.K + kPrepK - 1) / kPrepK);
+    const int r0 = (int)(blockIdx.y / segs) * kPrepRows + warp;
+    const int64_t k = (int64_t)(blockIdx.y % segs) * kPrepK + 16 * lane;
     const bool in_k = k < p.K;   // K is a multiple of 128: the 8 lanes of a stage agree
     uint8_t* out = p.out + ((int64_t)blockIdx.x * p.kt + k / 128) * p.chunk;
     const int unit = lane & 7;   // 16-byte unit of the stage's row
-    for (int r = warp; r < nrows; r += kPrepThreads / 32) {
+    uint4 in[2][2] = {};
+    bool wrong = false;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int r = r0 + 8 * i;
+        if (r >= nrows) break;
         int64_t row = s0 + r;
         if (p.rows) {
             const int32_t v = p.rows[s0 + r];
-            const bool in = v >= 0 && v < p.x_rows;
-            if (!in) raise_status(UW_ERR_DEVICE);
-            row = in ? v : 0;
+            const bool ok = v >= 0 && v < p.x_rows;
+            wrong |= !ok;
+            row = ok ? v : 0;
         }
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
         if (in_k) {
             const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k);
-            a = __ldg(src);
-            b = __ldg(src + 1);
+            in[i][0] = __ldg(src);
+            in[i][1] = __ldg(src + 1);
         }
+    }
+    if (wrong) raise_status(UW_ERR_DEVICE);
+#pragma unroll
+    for (int i2 = 0; i2 < 2; i2++) {
+        const int r = r0 + 8 * i2;
+        if (r >= nrows) break;
+        const uint4 a = in[i2][0], b = in[i2][1];
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         float v[16];
         uint32_t top = 0;
@@ -1163,7 +1177,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
         q.chunk = h.chunk;
         q.out = prep;
         if (src == kGroupMx8)
-            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK)), kPrepThreads, tab, s, q);
+            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows))), kPrepThreads, tab, s, q);
         else
             e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), kPrepThreads, 0, s, q);
         if (e != cudaSuccess) return e;

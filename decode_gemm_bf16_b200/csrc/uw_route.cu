@@ -438,26 +438,27 @@ __global__ void __launch_bounds__(kCombineThreads, IN32 ? 2 : 4) k_combine(const
     const int n = p.N - c < 8 ? (int)(p.N - c) : 8;
     float acc[8] = {};
     for (int j0 = 0; j0 < p.k; j0 += kCombineAhead) {
+        // all positions, then all rows: nothing in between that the loads would wait for
         Cols<IN32> z[kCombineAhead];
         float w[kCombineAhead];
+        int32_t s[kCombineAhead];
 #pragma unroll
         for (int j = 0; j < kCombineAhead; j++) {
-            int32_t s = -1;
-            w[j] = 0.0f;
-            if (j0 + j < p.k) {
-                s = __ldg(p.pos + t * p.k + j0 + j);
-                w[j] = __ldg(p.weights + t * p.k + j0 + j);
-            }
-            if (s >= p.slots) {
-                raise_status(UW_ERR_DEVICE);
-                s = -1;
-            }
-            z[j].a = z[j].b = make_uint4(0, 0, 0, 0);
-            if (s >= 0) load_cols<IN32>(p.Z, s * p.N + c, n, vec, z[j]);
-            else w[j] = 0.0f;
+            s[j] = j0 + j < p.k ? __ldg(p.pos + t * p.k + j0 + j) : -1;
+            w[j] = j0 + j < p.k ? __ldg(p.weights + t * p.k + j0 + j) : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < kCombineAhead; j++) add_cols<IN32>(z[j], w[j], acc);
+        for (int j = 0; j < kCombineAhead; j++) {
+            z[j].a = z[j].b = make_uint4(0, 0, 0, 0);
+            if (s[j] >= 0 && s[j] < p.slots) load_cols<IN32>(p.Z, s[j] * p.N + c, n, vec, z[j]);
+        }
+        bool wrong = false;
+#pragma unroll
+        for (int j = 0; j < kCombineAhead; j++) {
+            wrong |= s[j] >= p.slots;
+            add_cols<IN32>(z[j], s[j] < 0 || s[j] >= p.slots ? 0.0f : w[j], acc);
+        }
+        if (wrong) raise_status(UW_ERR_DEVICE);
     }
     const int64_t at = t * p.N + c;
     if (OUT32) {
