@@ -220,13 +220,11 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// 512 bytes of scales (32 rows x 16 bytes) -> 4 columns of tensor memory, in
-// every quarter of the lanes.
-__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem) {
+// 512 bytes of scales (32 rows x 16 bytes) at shared address 16 * (smem16 %
+// 2^14) -> 4 columns of tensor memory, in every quarter of the lanes.
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem16) {
     // rows of 16 bytes in 8-row groups of 128 bytes, no swizzle
-    uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu);
-    d |= (uint64_t)(128u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
+    const uint64_t d = ((uint64_t)((128u >> 4) | (1u << 14)) << 32) | (smem16 & 0x3FFFu);
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 
@@ -347,38 +345,102 @@ __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int64_
 // k of a stage.
 constexpr int stage_k(int src) { return src == kGroupMx8 ? 128 : src == kGroupMxMx ? 256 : 64; }
 
-// Bytes that a stage of tile t receives.
-template <int SRC>
-__device__ __forceinline__ uint32_t stage_tx(const GroupParams& p, const Tile& t) {
-    const int nN = mma_n<SRC>(t.rows);
-    uint32_t x = (uint32_t)((nN + p.box - 1) / p.box * p.box) * 128u;
-    if (SRC == kGroupMx8) x = (uint32_t)nN * 128u;
-    else if (p.rows) x = (uint32_t)((t.rows + 3) / 4) * 512u;
-    // the unpacking load counts the packed bytes of its rows
-    return (uint32_t)kTileN * (SRC == kGroupMx ? 32u : SRC == kGroupMx8 ? 64u : 128u) + p.sf_a_bytes * (p.up ? 2u : 1u) + p.sf_b_bytes + x;
+// Wait of a role's single thread: one test where the phase is complete, the
+// bounded wait out of line.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
+    return mbar_wait(bar, parity, timeout, abort);
+}
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
+    return mbar_try_wait(bar, parity, 1000) || wait_slow(bar, parity, timeout, abort);
 }
 
-// Weight rows (64 of each matrix, or 128) and their scales of one stage.
+// What the producer thread loads for the stages of one tile, from k step kt on:
+// everything that changes from stage to stage is advanced, not computed anew.
 template <int SRC>
-__device__ __forceinline__ void load_weights(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
-                                             const Tile& t, int kt, uint32_t st, uint32_t fb) {
-    constexpr int KB = stage_k(SRC);
-    constexpr uint32_t kARow = SRC == kGroupMx ? 32 : 128;
-    const int n0 = t.n * (p.up ? kTileN / 2 : kTileN);
-    const int64_t wrow = (int64_t)t.e * p.N + n0;
-    const int ax = SRC == kGroupBf16 || SRC == kGroupMx8 ? kt * KB : kt * (KB / 2);   // codes unpacked by the TMA count as elements
-    tma_load_2d(st, &tm_w, ax, (int)wrow, fb);
-    tma_load_2d(st + kTileN / 2 * kARow, p.up ? &tm_u : &tm_w, ax, (int)(p.up ? wrow : wrow + kTileN / 2), fb);
-    if (SRC != kGroupBf16) {
-        // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
-        const int64_t at = ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes +
-                           (SRC == kGroupMxMx  ? (int64_t)kt * kMxTileBytes
-                            : SRC == kGroupMx8 ? (int64_t)kt * (kMxTileBytes / 2)
-                                               : (int64_t)(kt >> 1) * (kMxTileBytes / 2));
-        bulk_load(st + p.off_s, p.sw + at, p.sf_a_bytes, fb);
-        if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, p.su + at, p.sf_a_bytes, fb);
+struct Feed {
+    static constexpr int KB = stage_k(SRC);
+    static constexpr uint32_t kARow = SRC == kGroupMx ? 32 : 128;
+    const CUtensorMap* second;   // map of the tile's rows 64..127
+    int ax, w0, w1;              // column and rows of the weight boxes
+    const uint8_t* s0;           // scales of the stage's weights (and of `up`)
+    const uint8_t* s1;
+    int half;                    // kGroupMx: a scale half tile (128 k) serves two stages
+    const uint8_t* x0;           // split rows, or the scales of 128 rows of X (and of the next 128)
+    const uint8_t* x1;
+    int bx, y, boxes, gathers;
+    uint32_t x_bytes, tx;
+
+    __device__ __forceinline__ Feed(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u, const Tile& t, int kt) {
+        const int n0 = t.n * (p.up ? kTileN / 2 : kTileN), nN = mma_n<SRC>(t.rows);
+        w0 = t.e * (int)p.N + n0;   // E N is below 2^31
+        w1 = p.up ? w0 : w0 + kTileN / 2;
+        second = p.up ? &tm_u : &tm_w;
+        // codes that the TMA unpacks count as elements of a box, packed ones as bytes
+        ax = kt * (SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2);
+        bx = kt * (SRC == kGroupMxMx ? KB / 2 : KB);
+        y = (int)t.s0;
+        boxes = (nN + p.box - 1) / p.box;
+        gathers = p.rows ? (t.rows + 3) / 4 : 0;
+        x_bytes = SRC == kGroupMx8 ? (uint32_t)nN * 128u : p.rows ? (uint32_t)gathers * 512u : (uint32_t)(boxes * p.box) * 128u;
+        // the unpacking load counts the packed bytes of its rows
+        tx = (uint32_t)kTileN * (SRC == kGroupMx8 ? 64u : kARow) + p.sf_a_bytes * (p.up ? 2u : 1u) + p.sf_b_bytes + x_bytes;
+        s0 = s1 = x0 = x1 = nullptr;
+        half = 0;
+        if (SRC != kGroupBf16) {
+            // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
+            const int64_t at = ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes +
+                               (SRC == kGroupMxMx  ? (int64_t)kt * kMxTileBytes
+                                : SRC == kGroupMx8 ? (int64_t)kt * (kMxTileBytes / 2)
+                                                   : (int64_t)(kt >> 1) * (kMxTileBytes / 2));
+            half = kt & 1;
+            s0 = p.sw + at;
+            if (p.up) s1 = p.su + at;
+        }
+        if (SRC == kGroupMx8) x0 = p.prep + (t.m * p.kt + kt) * p.prep_chunk;
+        if (SRC == kGroupMxMx) {
+            // a row tile past the last reads the last one again (rows past the end: never stored)
+            const int64_t rt = t.s0 / kMxTileRows, last = (p.x_rows - 1) / kMxTileRows;
+            x0 = p.sx + (rt * p.k_tiles + kt) * kMxTileBytes;
+            x1 = p.sx + ((rt < last ? rt + 1 : last) * p.k_tiles + kt) * kMxTileBytes;
+        }
     }
-}
+    __device__ __forceinline__ void weights(const GroupParams& p, const CUtensorMap& tm_w, uint32_t st, uint32_t fb) {
+        mbar_arrive_expect_tx(fb, tx);
+        tma_load_2d(st, &tm_w, ax, w0, fb);
+        tma_load_2d(st + kTileN / 2 * kARow, second, ax, w1, fb);
+        ax += SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2;
+        if (SRC != kGroupBf16) {
+            bulk_load(st + p.off_s, s0, p.sf_a_bytes, fb);
+            if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, s1, p.sf_a_bytes, fb);
+            const uint32_t step = SRC == kGroupMx && !half ? 0 : p.sf_a_bytes;
+            s0 += step;
+            s1 += step;
+            if (SRC == kGroupMx) half ^= 1;
+        }
+    }
+    __device__ __forceinline__ void rows(const GroupParams& p, const CUtensorMap& tm_x, uint32_t st, uint32_t fb,
+                                         const int4 (&idx)[8]) {
+        if (SRC == kGroupMx8) {   // scales and rows, one run in both memories
+            bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes + x_bytes, fb);
+            x0 += p.prep_chunk;
+            return;
+        }
+        if (SRC == kGroupMxMx) {
+            bulk_load(st + p.off_b - p.sf_b_bytes, x0, kMxTileBytes, fb);
+            if (p.sf_b_bytes > kMxTileBytes) bulk_load(st + p.off_b - kMxTileBytes, x1, kMxTileBytes, fb);
+            x0 += kMxTileBytes;
+            x1 += kMxTileBytes;
+        }
+        if (gathers) {
+#pragma unroll
+            for (int g = 0; g < 8; g++)
+                if (g < gathers) tma_gather4(st + p.off_b + (uint32_t)g * 512u, &tm_x, bx, idx[g], fb);
+        } else {
+            for (int b = 0; b < boxes; b++) tma_load_2d(st + p.off_b + (uint32_t)(b * p.box) * 128u, &tm_x, bx, y + b * p.box, fb);
+        }
+        bx += SRC == kGroupMxMx ? KB / 2 : KB;
+    }
+};
 
 template <int SRC>
 __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
@@ -453,147 +515,147 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
 
     if (warp == kProd) {
         // ------------------------------------------------------------ TMA producer
-        const bool leader = elect_one();
+        // One thread walks the stages.
+        if (elect_one()) {
         int64_t q = 0, pre = 0;
         Seg sg;
         if (p.early) {
             // the first stages' weights and scales, before the wait on the preparing kernel
             Walk w0(pl, blockIdx.x);
             while (pre < p.S && w0.next(pl, p.kt, sg)) {
-                const Tile t = locate(p, pl, sg.tile);
+                Feed<SRC> f(p, tm_w, tm_u, locate(p, pl, sg.tile), sg.kt0);
                 for (int kt = sg.kt0; kt < sg.kt1 && pre < p.S; kt++, pre++)
-                    if (leader) {
-                        mbar_arrive_expect_tx(full + 8 * (uint32_t)pre, stage_tx<SRC>(p, t));
-                        load_weights<SRC>(p, tm_w, tm_u, t, kt, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre);
-                    }
+                    f.weights(p, tm_w, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre);
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
         }
         Walk wk(pl, blockIdx.x);
-        Ring r;
+        int slot = 0;
+        uint32_t ph = 1, st = base, fb = full;
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
             const Tile t = locate(p, pl, sg.tile);
-            const int nN = mma_n<SRC>(t.rows);
-            const int boxes = (nN + p.box - 1) / p.box;
-            int4 idx = {};
-            if (p.rows && lane < (t.rows + 3) / 4) {
-                // four rows a lane; past the tile's end its last row again (never stored)
-                int* ip = &idx.x;
+            int4 idx[8];
+            if (p.rows) {
+                // four rows a request; past the tile's end its last row again (never stored)
+                int* ip = &idx[0].x;
+                bool wrong = false;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int at = 4 * lane + i;
-                    const int32_t v = p.rows[t.s0 + (at < t.rows ? at : t.rows - 1)];
+                for (int i = 0; i < 32; i++) {
+                    const int32_t v = p.rows[t.s0 + (i < t.rows ? i : t.rows - 1)];
                     const bool in = v >= 0 && v < p.x_rows;
-                    if (!in) raise_status(UW_ERR_DEVICE);
+                    wrong |= !in;
                     ip[i] = in ? v : 0;
                 }
+                if (wrong) raise_status(UW_ERR_DEVICE);
             }
-            for (int kt = sg.kt0; kt < sg.kt1; kt++, q++, r.advance(p.S)) {
-                const uint32_t st = base + (uint32_t)r.i * p.stage_bytes, fb = full + 8 * r.i;
+            Feed<SRC> f(p, tm_w, tm_u, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0);
+            Feed<SRC> x(p, tm_w, tm_u, t, sg.kt0);
+            for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                 if (q >= pre) {
-                    if (!mbar_wait(empty + 8 * r.i, r.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
-                    if (leader) {
-                        mbar_arrive_expect_tx(fb, stage_tx<SRC>(p, t));
-                        load_weights<SRC>(p, tm_w, tm_u, t, kt, st, fb);
-                    }
+                    if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
+                    f.weights(p, tm_w, st, fb);
                 }
-                if (SRC == kGroupMx8) {
-                    // scales and rows of the stage, one run in both memories
-                    if (leader)
-                        bulk_load(st + p.off_b - p.sf_b_bytes, p.prep + (t.m * p.kt + kt) * p.prep_chunk,
-                                  p.sf_b_bytes + (uint32_t)nN * 128u, fb);
-                } else if (p.rows) {
-                    __syncwarp();
-                    if (lane < (t.rows + 3) / 4) tma_gather4(st + p.off_b + (uint32_t)lane * 512u, &tm_x, kt * KB, idx, fb);
-                } else if (leader) {
-                    if (SRC == kGroupMxMx) {
-                        const int64_t rt = t.s0 / kMxTileRows;
-                        for (uint32_t i = 0; i < p.sf_b_bytes / kMxTileBytes; i++) {
-                            // a row tile past the last reads the last one again (rows past the end: never stored)
-                            const int64_t last = (p.x_rows - 1) / kMxTileRows, at = rt + i < last ? rt + i : last;
-                            bulk_load(st + p.off_b - p.sf_b_bytes + i * kMxTileBytes,
-                                      p.sx + (at * p.k_tiles + kt) * kMxTileBytes, kMxTileBytes, fb);
-                        }
-                    }
-                    for (int b = 0; b < boxes; b++)
-                        tma_load_2d(st + p.off_b + (uint32_t)(b * p.box) * 128u, &tm_x, kt * (SRC == kGroupMxMx ? KB / 2 : KB),
-                                    (int)(t.s0 + b * p.box), fb);
+                x.rows(p, tm_x, st, fb, idx);
+                st += p.stage_bytes;
+                fb += 8;
+                if (++slot == p.S) {
+                    slot = 0;
+                    ph ^= 1u;
+                    st = base;
+                    fb = full;
                 }
             }
         }
         if (!ok)   // every load already issued lands before the CTA exits
             for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
                 mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
+        }
+        __syncwarp();
     } else if (warp == kMma) {
         // ------------------------------------------------------------ MMA issue
-        const bool leader = elect_one();
+        // One thread walks the stages; descriptors and barriers advance with the slot.
+        if (elect_one()) {
+        constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // sw128_desc's upper word
+        const uint32_t lo0 = ((base >> 4) & 0x3FFFu) | (1u << 16), lo_step = p.stage_bytes >> 4, lo_b = p.off_b >> 4;
+        auto desc = [](uint32_t lo) { return ((uint64_t)kHi << 32) | lo; };
         Walk wk(pl, blockIdx.x);
         Seg sg;
-        Ring r, rt, ra;
+        Ring rt, ra;
+        int slot = 0;
+        uint32_t ph = 0, fb = full, lo = lo0, sf = tmem + p.sf_col0;
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
-            const Tile t = locate(p, pl, sg.tile);
-            const int nN = mma_n<SRC>(t.rows);
-            const uint32_t idesc = mma_idesc_bf16(kTileN, nN);
-            if (!mbar_wait(acce + 8 * ra.i, ra.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
+            const int nN = mma_n<SRC>(locate(p, pl, sg.tile).rows);
+            const uint32_t idesc = SRC == kGroupMx8 ? idesc_mx8(nN, 0) : SRC == kGroupMxMx ? idesc_mx(nN, 0) : mma_idesc_bf16(kTileN, nN);
+            if (!wait_one(acce + 8 * ra.i, ra.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const uint32_t acc = tmem + (uint32_t)ra.i * p.acc_w;
-            for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
-                if (kRe && !mbar_wait(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (SRC == kGroupMx8 && p.up && !mbar_wait(mixed + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
+            uint32_t more = 0;   // 0: the tile's first MMA overwrites
+            for (int kt = sg.kt0; kt < sg.kt1; kt++) {
+                if (kRe && !wait_one(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
+                if (SRC == kGroupMx8 && p.up && !wait_one(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
+                if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                if (leader) {
-                    const uint32_t st = base + (uint32_t)r.i * p.stage_bytes;
-                    const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + p.off_b);
-                    if (kScaled) {
-                        // scales of the stage, 4 columns per 512 bytes: weights, then rows
-                        const uint32_t sfa = tmem + p.sf_col0 + (uint32_t)r.i * p.sf_slot, ss = st + p.off_s;
-                        const uint32_t sfb = sfa + (SRC == kGroupMxMx ? 8u : 4u), sb = st + p.off_b - p.sf_b_bytes;
-                        if (SRC == kGroupMxMx) {
-                            const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
+                if (kScaled) {
+                    // scales of the stage, 4 columns per 512 bytes: weights, then rows
+                    const uint32_t ss = lo + (p.off_s >> 4), sb = lo + lo_b - (p.sf_b_bytes >> 4);
+                    const uint32_t sfb = sf + (SRC == kGroupMxMx ? 8u : 4u);
+                    if (SRC == kGroupMxMx) {
+                        const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
 #pragma unroll
-                            for (uint32_t h = 0; h < 2; h++) {
-                                tc_copy_scales(sfa + 4u * h, ss + 512u * h);
-                                for (uint32_t i = 0; i < nb; i++)
-                                    tc_copy_scales(sfb + 4u * (h * nb + i), sb + kMxTileBytes * i + 512u * h);
-                            }
-#pragma unroll
-                            for (uint32_t j = 0; j < 4; j++)
-                                tc_mma_mx(acc, ad + 2u * j, bd + 2u * j, idesc_mx(nN, 2u * (j & 1u)), sfa + 4u * (j >> 1),
-                                          sfb + 4u * nb * (j >> 1), kt > sg.kt0 || j > 0 ? 1u : 0u);
-                        } else {
-                            tc_copy_scales(sfa, p.up ? ss + 1024u : ss);
-                            for (uint32_t i = 0; i < p.sf_b_bytes / 512u; i++) tc_copy_scales(sfb + 4u * i, sb + 512u * i);
-#pragma unroll
-                            for (uint32_t j = 0; j < 4; j++)
-                                tc_mma_mx8(acc, ad + 2u * j, bd + 2u * j, idesc_mx8(nN, j), sfa, sfb,
-                                           kt > sg.kt0 || j > 0 ? 1u : 0u);
+                        for (uint32_t h = 0; h < 2; h++) {
+                            tc_copy_scales(sf + 4u * h, ss + 32u * h);
+                            tc_copy_scales(sfb + 4u * h * nb, sb + 32u * h);
+                            if (nb > 1) tc_copy_scales(sfb + 4u * (h * nb + 1), sb + 64u + 32u * h);
                         }
+#pragma unroll
+                        for (uint32_t j = 0; j < 4; j++, more = 1)
+                            tc_mma_mx(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
+                                      sf + 4u * (j >> 1), sfb + 4u * nb * (j >> 1), more);
                     } else {
-                        const uint32_t ta = tmem + p.a_col0 + (uint32_t)(KB / 2) * (uint32_t)rt.i;
+                        tc_copy_scales(sf, p.up ? ss + 64u : ss);
+                        tc_copy_scales(sfb, sb);
+                        if (p.sf_b_bytes > 512u) tc_copy_scales(sfb + 4u, sb + 32u);
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t more = kt > sg.kt0 || j > 0 ? 1u : 0u;
-                            if (kRe)
-                                tc_mma_tmem_a(acc, ta + 8u * (uint32_t)j, bd + 2u * j, idesc, more);
-                            else
-                                tc_mma(acc, ad + 2u * j, bd + 2u * j, idesc, more);
-                        }
+                        for (uint32_t j = 0; j < 4; j++, more = 1)
+                            tc_mma_mx8(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + j * ((1u << 4) | (1u << 29)), sf, sfb,
+                                       more);
                     }
-                    tc_commit(empty + 8 * r.i);
-                    if (kRe) tc_commit(tfree + 8 * rt.i);
+                    sf += p.sf_slot;
+                } else {
+                    const uint32_t ta = tmem + p.a_col0 + (uint32_t)(KB / 2) * (uint32_t)rt.i;
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; j++, more = 1) {
+                        if (kRe)
+                            tc_mma_tmem_a(acc, ta + 8u * j, desc(lo + lo_b + 2u * j), idesc, more);
+                        else
+                            tc_mma(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc, more);
+                    }
                 }
-                if (kRe) rt.advance(p.T);
+                tc_commit(fb + 8 * kMaxS);   // empty
+                if (kRe) {
+                    tc_commit(tfree + 8 * rt.i);
+                    rt.advance(p.T);
+                }
+                lo += lo_step;
+                fb += 8;
+                if (++slot == p.S) {
+                    slot = 0;
+                    ph ^= 1u;
+                    lo = lo0;
+                    fb = full;
+                    sf = tmem + p.sf_col0;
+                }
             }
             if (!ok) break;
-            if (leader) tc_commit(accf + 8 * ra.i);
+            tc_commit(accf + 8 * ra.i);
             ra.advance(p.nacc);
         }
         // drain the tensor core before tensor memory is released
-        if (leader) tc_commit(fin);
+        tc_commit(fin);
         mbar_wait(fin, 0, p.timeout, nullptr);
+        }
         __syncwarp();
     } else if (SRC == kGroupMx8 && warp == kMix) {
         // ------------------------------------------------------------ scales of two weights
