@@ -118,7 +118,8 @@ struct Plan {
     const int32_t* count;    // [E] slots
     int64_t tiles, whole;    // tiles; tiles dealt out whole (the first ones)
     int64_t units;           // k steps of the cut tiles
-    int ps;                  // CTAs that share them
+    int ps;                  // of the P workers (CTAs or pairs), those that share them
+    int P;
 };
 
 struct Seg {
@@ -132,11 +133,11 @@ struct Tile {
     int64_t m;               // the slot tile's number among all
 };
 
-// Units of CTA b's range start here; owner of a unit.
+// Units of worker b's range start here; owner of a unit.
 __device__ __forceinline__ int64_t unit_begin(int64_t b, const Plan& pl) { return b * pl.units / pl.ps; }
 __device__ __forceinline__ int unit_owner(int64_t u, const Plan& pl) { return (int)(((u + 1) * pl.ps - 1) / pl.units); }
 
-// A CTA's segments: its range of the cut tiles, then its whole tiles.
+// A worker's segments: its range of the cut tiles, then its whole tiles.
 struct Walk {
     int64_t u, ue, t;
     __device__ __forceinline__ Walk(const Plan& pl, int b) {
@@ -160,7 +161,7 @@ struct Walk {
             s.tile = t;
             s.kt0 = 0;
             s.kt1 = kt;
-            t += gridDim.x;
+            t += pl.P;
             return true;
         }
         return false;
@@ -222,27 +223,51 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
 
 // 512 bytes of scales (32 rows x 16 bytes) at shared address 16 * (smem16 %
 // 2^14) -> 4 columns of tensor memory, in every quarter of the lanes.
+template <int CG>
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem16) {
     // rows of 16 bytes in 8-row groups of 128 bytes, no swizzle
     const uint64_t d = ((uint64_t)((128u >> 4) | (1u << 14)) << 32) | (smem16 & 0x3FFFu);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    if (CG == 1) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 
 // D (+)= A * B^T with e2m1 operands and one e8m0 scale per 32 k (K = 64).
+template <int CG>
 __device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t acc) {
-    asm volatile(
+    if (CG == 1)
+        asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");
+    else
+        asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if (CG == 1)
+        tc_mma(d_tmem, ad, bd, idesc, acc);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
 }
 
 // Instruction descriptor of kind::mxf4: both operands e2m1, scales e8m0, both
-// K-major, M = 128; `id` (0 or 2) picks the scale bytes' half word.
-__device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t id) {
-    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+// K-major, M = 128 a CTA; `id` (0 or 2) picks the scale bytes' half word.
+__device__ __forceinline__ uint32_t idesc_mx(int CG, int N, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)CG << 27) | (id << 29);
 }
 
 // 32 codes with scale byte s -> 16 BF16 pairs.  The eight magnitudes times
@@ -279,27 +304,38 @@ __device__ __forceinline__ void rebuild32(const uint4 c, uint32_t s, uint32_t (&
 __device__ __forceinline__ uint32_t sw32(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
 
 // D (+)= A * B^T, A e2m1 (a byte each), B e4m3, one e8m0 scale per 32 k (K = 32).
+template <int CG>
 __device__ __forceinline__ void tc_mma_mx8(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                            uint32_t sfb, uint32_t acc) {
-    asm volatile(
+    if (CG == 1)
+        asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");
+    else
+        asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
 }
 
 // Instruction descriptor of kind::mxf8f6f4: A e2m1, B e4m3, scales e8m0, both
-// K-major, M = 128; `id` (0..3) picks the scale byte.
-__device__ __forceinline__ uint32_t idesc_mx8(int N, uint32_t id) {
-    return (id << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29);
+// K-major, M = 128 a CTA; `id` (0..3) picks the scale byte.
+__device__ __forceinline__ uint32_t idesc_mx8(int CG, int N, uint32_t id) {
+    return (id << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)CG << 27) | (id << 29);
 }
 
 // Columns of the MMA's N for a tile of `rows` slots: the rows rounded up to
-// 16; two of them (hi, lo) per row rounded up to 8 for split rows.
-template <int SRC>
+// 16; two of them (hi, lo) per row rounded up to 8 for split rows.  A pair
+// takes multiples of 32, 16 a CTA.
+template <int SRC, int CG>
 __device__ __forceinline__ int mma_n(int rows) {
-    return SRC == kGroupMx8 ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;
+    constexpr int step = (SRC == kGroupMx8 ? 8 : 16) * CG;
+    return (rows + step - 1) / step * step * (SRC == kGroupMx8 ? 2 : 1);
 }
 
 // The tile list from the offsets: tables cum[E + 1], begin[E], count[E] in
@@ -345,6 +381,62 @@ __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int64_
 // k of a stage.
 constexpr int stage_k(int src) { return src == kGroupMx8 ? 128 : src == kGroupMxMx ? 256 : 64; }
 
+// ---- pairs of CTAs (cta_group::2): forms of the shared helpers
+template <int CG>
+__device__ __forceinline__ void pair_alloc(uint32_t dst, uint32_t cols) {
+    if (CG == 1) {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t cols) {
+    if (CG == 1) tmem_dealloc(taddr, cols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+// Arrive once on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    if (CG == 1)
+        tc_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+}
+// Address of this CTA's `bar` in the pair's first CTA, and an arrival there.
+__device__ __forceinline__ uint32_t in_first(uint32_t bar) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
+    return a;
+}
+// arrive_at orders nothing: it passes on that copies have landed, which the
+// tensor cores then read where they are.  (With .release.cluster a stage took
+// 1600 cycles instead of 560.)
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void release_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool test_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Wait of a role's single thread: one test where the phase is complete, the
 // bounded wait out of line.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
@@ -353,10 +445,27 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t t
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
     return mbar_try_wait(bar, parity, 1000) || wait_slow(bar, parity, timeout, abort);
 }
+// The same for a barrier on which the pair's other CTA arrives too.
+template <int CG>
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
+    if (CG == 1) return wait_one(bar, parity, timeout, abort);
+    if (test_cluster(bar, parity)) return true;
+    const uint64_t deadline = globaltimer() + timeout;
+    for (uint32_t i = 1;; i++) {
+        if (test_cluster(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            if (*abort) return false;
+            if (globaltimer() > deadline) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
 
 // What the producer thread loads for the stages of one tile, from k step kt on:
 // everything that changes from stage to stage is advanced, not computed anew.
-template <int SRC>
+template <int SRC, int CG>
 struct Feed {
     static constexpr int KB = stage_k(SRC);
     static constexpr uint32_t kARow = SRC == kGroupMx ? 32 : 128;
@@ -368,17 +477,19 @@ struct Feed {
     const uint8_t* x0;           // split rows, or the scales of 128 rows of X (and of the next 128)
     const uint8_t* x1;
     int bx, y, boxes, gathers;
-    uint32_t x_bytes, tx;
+    uint32_t x_bytes, x_at, tx;  // X: bytes, and where this CTA's half starts
 
-    __device__ __forceinline__ Feed(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u, const Tile& t, int kt) {
-        const int n0 = t.n * (p.up ? kTileN / 2 : kTileN), nN = mma_n<SRC>(t.rows);
+    __device__ __forceinline__ Feed(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u, const Tile& t, int kt,
+                                    int rank) {
+        const int n0 = (t.n * CG + rank) * (p.up ? kTileN / 2 : kTileN), nN = mma_n<SRC, CG>(t.rows) / CG;
         w0 = t.e * (int)p.N + n0;   // E N is below 2^31
         w1 = p.up ? w0 : w0 + kTileN / 2;
         second = p.up ? &tm_u : &tm_w;
         // codes that the TMA unpacks count as elements of a box, packed ones as bytes
         ax = kt * (SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2);
         bx = kt * (SRC == kGroupMxMx ? KB / 2 : KB);
-        y = (int)t.s0;
+        y = (int)t.s0 + rank * nN;
+        x_at = p.sf_b_bytes + (uint32_t)(rank * nN) * 128u;
         boxes = (nN + p.box - 1) / p.box;
         gathers = p.rows ? (t.rows + 3) / 4 : 0;
         x_bytes = SRC == kGroupMx8 ? (uint32_t)nN * 128u : p.rows ? (uint32_t)gathers * 512u : (uint32_t)(boxes * p.box) * 128u;
@@ -388,7 +499,9 @@ struct Feed {
         half = 0;
         if (SRC != kGroupBf16) {
             // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
-            const int64_t at = ((int64_t)t.e * p.w_row_tiles + n0 / kMxTileRows) * p.k_tiles * kMxTileBytes +
+            // (the second CTA of a pair may stand past the last row tile)
+            const int64_t row_tile = n0 / kMxTileRows < p.w_row_tiles ? n0 / kMxTileRows : p.w_row_tiles - 1;
+            const int64_t at = ((int64_t)t.e * p.w_row_tiles + row_tile) * p.k_tiles * kMxTileBytes +
                                (SRC == kGroupMxMx  ? (int64_t)kt * kMxTileBytes
                                 : SRC == kGroupMx8 ? (int64_t)kt * (kMxTileBytes / 2)
                                                    : (int64_t)(kt >> 1) * (kMxTileBytes / 2));
@@ -421,7 +534,12 @@ struct Feed {
     __device__ __forceinline__ void rows(const GroupParams& p, const CUtensorMap& tm_x, uint32_t st, uint32_t fb,
                                          const int4 (&idx)[8]) {
         if (SRC == kGroupMx8) {   // scales and rows, one run in both memories
-            bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes + x_bytes, fb);
+            if (CG == 1) {
+                bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes + x_bytes, fb);
+            } else {   // all columns' scales, this CTA's half of the rows
+                bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes, fb);
+                bulk_load(st + p.off_b, x0 + x_at, x_bytes, fb);
+            }
             x0 += p.prep_chunk;
             return;
         }
@@ -442,7 +560,7 @@ struct Feed {
     }
 };
 
-template <int SRC>
+template <int SRC, int CG>
 __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
                                            const GroupParams& p) {
     constexpr int KB = stage_k(SRC);
@@ -453,16 +571,20 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ctrl_off);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxS, recon = empty + 8 * kMaxS, tfree = recon + 8 * kMaxT;
-    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxS + 2 * kMaxT + 5);
+    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8, peer = mixed + 8 * kMaxS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * kMaxS + 2 * kMaxT + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* cum = reinterpret_cast<int32_t*>(smem + p.tab_off);
     int32_t* begin = cum + p.E + 1;
     int32_t* count = begin + p.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // A pair of CTAs works as one on 256 weight rows: each holds its 128 rows
+    // and half of the tile's X; the first issues the MMAs of both.
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)(blockIdx.x / CG);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.S; s++) {
+            mbar_init(peer + 8 * s, 1);
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
             mbar_init(mixed + 8 * s, 1);
@@ -473,16 +595,13 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         }
         for (int a = 0; a < 2; a++) {
             mbar_init(accf + 8 * a, 1);
-            mbar_init(acce + 8 * a, 4);
+            mbar_init(acce + 8 * a, 4 * CG);
         }
         mbar_init(fin, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kMma) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == kMma) pair_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
     if (warp == kProd && lane == 0) {
         tma_prefetch_desc(&tm_x);
         tma_prefetch_desc(&tm_w);
@@ -494,6 +613,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count);
+    if (CG == 2) cluster_sync();   // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -504,7 +624,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     pl.count = count;
     pl.tiles = cum[p.E];
     {
-        const int64_t P = gridDim.x, rounds = pl.tiles / P;
+        const int64_t P = gridDim.x / CG, rounds = pl.tiles / P;
+        pl.P = (int)P;
         pl.whole = pl.tiles % P == 0 ? pl.tiles : rounds > 1 ? (rounds - 1) * P : 0;
         pl.units = (pl.tiles - pl.whole) * p.kt;
         // a range shorter than two k steps costs more to join than it saves
@@ -521,15 +642,15 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         Seg sg;
         if (p.early) {
             // the first stages' weights and scales, before the wait on the preparing kernel
-            Walk w0(pl, blockIdx.x);
+            Walk w0(pl, worker);
             while (pre < p.S && w0.next(pl, p.kt, sg)) {
-                Feed<SRC> f(p, tm_w, tm_u, locate(p, pl, sg.tile), sg.kt0);
+                Feed<SRC, CG> f(p, tm_w, tm_u, locate(p, pl, sg.tile), sg.kt0, rank);
                 for (int kt = sg.kt0; kt < sg.kt1 && pre < p.S; kt++, pre++)
                     f.weights(p, tm_w, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre);
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
         }
-        Walk wk(pl, blockIdx.x);
+        Walk wk(pl, worker);
         int slot = 0;
         uint32_t ph = 1, st = base, fb = full;
         bool ok = true;
@@ -549,8 +670,9 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
                 if (wrong) raise_status(UW_ERR_DEVICE);
             }
-            Feed<SRC> f(p, tm_w, tm_u, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0);
-            Feed<SRC> x(p, tm_w, tm_u, t, sg.kt0);
+            Feed<SRC, CG> f(p, tm_w, tm_u, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0,
+                            rank);
+            Feed<SRC, CG> x(p, tm_w, tm_u, t, sg.kt0, rank);
             for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                 if (q >= pre) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
@@ -575,20 +697,44 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     } else if (warp == kMma) {
         // ------------------------------------------------------------ MMA issue
         // One thread walks the stages; descriptors and barriers advance with the slot.
-        if (elect_one()) {
+        if (CG == 2 && rank == 1) {
+            // the pair's second CTA tells the first which of its stages have landed
+            if (elect_one()) {
+                Walk wk(pl, worker);
+                Seg sg;
+                int slot = 0;
+                uint32_t ph = 0, fb = full;
+                const uint32_t to = in_first(peer) - full;
+                bool ok = true;
+                while (ok && wk.next(pl, p.kt, sg))
+                    for (int kt = sg.kt0; kt < sg.kt1; kt++) {
+                        if (SRC == kGroupMx8 && p.up && !wait_one(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
+                        if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
+                        arrive_at(fb + to);
+                        fb += 8;
+                        if (++slot == p.S) {
+                            slot = 0;
+                            ph ^= 1u;
+                            fb = full;
+                        }
+                    }
+            }
+        } else if (elect_one()) {
         constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // sw128_desc's upper word
         const uint32_t lo0 = ((base >> 4) & 0x3FFFu) | (1u << 16), lo_step = p.stage_bytes >> 4, lo_b = p.off_b >> 4;
         auto desc = [](uint32_t lo) { return ((uint64_t)kHi << 32) | lo; };
-        Walk wk(pl, blockIdx.x);
+        Walk wk(pl, worker);
         Seg sg;
         Ring rt, ra;
         int slot = 0;
         uint32_t ph = 0, fb = full, lo = lo0, sf = tmem + p.sf_col0;
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
-            const int nN = mma_n<SRC>(locate(p, pl, sg.tile).rows);
-            const uint32_t idesc = SRC == kGroupMx8 ? idesc_mx8(nN, 0) : SRC == kGroupMxMx ? idesc_mx(nN, 0) : mma_idesc_bf16(kTileN, nN);
-            if (!wait_one(acce + 8 * ra.i, ra.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
+            const int nN = mma_n<SRC, CG>(locate(p, pl, sg.tile).rows);
+            const uint32_t idesc = SRC == kGroupMx8    ? idesc_mx8(CG, nN, 0)
+                                   : SRC == kGroupMxMx ? idesc_mx(CG, nN, 0)
+                                                       : mma_idesc_bf16(CG * kTileN, nN);
+            if (!wait_pair<CG>(acce + 8 * ra.i, ra.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const uint32_t acc = tmem + (uint32_t)ra.i * p.acc_w;
             uint32_t more = 0;   // 0: the tile's first MMA overwrites
@@ -596,6 +742,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 if (kRe && !wait_one(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (SRC == kGroupMx8 && p.up && !wait_one(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
+                if (CG == 2 && !wait_pair<CG>(fb + (peer - full), ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (kScaled) {
                     // scales of the stage, 4 columns per 512 bytes: weights, then rows
@@ -605,21 +752,21 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                         const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
 #pragma unroll
                         for (uint32_t h = 0; h < 2; h++) {
-                            tc_copy_scales(sf + 4u * h, ss + 32u * h);
-                            tc_copy_scales(sfb + 4u * h * nb, sb + 32u * h);
-                            if (nb > 1) tc_copy_scales(sfb + 4u * (h * nb + 1), sb + 64u + 32u * h);
+                            tc_copy_scales<CG>(sf + 4u * h, ss + 32u * h);
+                            tc_copy_scales<CG>(sfb + 4u * h * nb, sb + 32u * h);
+                            if (nb > 1) tc_copy_scales<CG>(sfb + 4u * (h * nb + 1), sb + 64u + 32u * h);
                         }
 #pragma unroll
                         for (uint32_t j = 0; j < 4; j++, more = 1)
-                            tc_mma_mx(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
+                            tc_mma_mx<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
                                       sf + 4u * (j >> 1), sfb + 4u * nb * (j >> 1), more);
                     } else {
-                        tc_copy_scales(sf, p.up ? ss + 64u : ss);
-                        tc_copy_scales(sfb, sb);
-                        if (p.sf_b_bytes > 512u) tc_copy_scales(sfb + 4u, sb + 32u);
+                        tc_copy_scales<CG>(sf, p.up ? ss + 64u : ss);
+                        tc_copy_scales<CG>(sfb, sb);
+                        if (p.sf_b_bytes > 512u) tc_copy_scales<CG>(sfb + 4u, sb + 32u);
 #pragma unroll
                         for (uint32_t j = 0; j < 4; j++, more = 1)
-                            tc_mma_mx8(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + j * ((1u << 4) | (1u << 29)), sf, sfb,
+                            tc_mma_mx8<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + j * ((1u << 4) | (1u << 29)), sf, sfb,
                                        more);
                     }
                     sf += p.sf_slot;
@@ -630,10 +777,10 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                         if (kRe)
                             tc_mma_tmem_a(acc, ta + 8u * j, desc(lo + lo_b + 2u * j), idesc, more);
                         else
-                            tc_mma(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc, more);
+                            tc_mma_bf16<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc, more);
                     }
                 }
-                tc_commit(fb + 8 * kMaxS);   // empty
+                pair_commit<CG>(fb + 8 * kMaxS);   // empty
                 if (kRe) {
                     tc_commit(tfree + 8 * rt.i);
                     rt.advance(p.T);
@@ -649,11 +796,11 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
             }
             if (!ok) break;
-            tc_commit(accf + 8 * ra.i);
+            pair_commit<CG>(accf + 8 * ra.i);
             ra.advance(p.nacc);
         }
         // drain the tensor core before tensor memory is released
-        tc_commit(fin);
+        pair_commit<CG>(fin);
         mbar_wait(fin, 0, p.timeout, nullptr);
         }
         __syncwarp();
@@ -663,7 +810,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
         // either into the 16 bytes that tensor memory takes for lane l.
         if (p.up) {
-            Walk wk(pl, blockIdx.x);
+            Walk wk(pl, worker);
             Seg sg;
             Ring r;
             bool ok = true;
@@ -672,7 +819,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
                     if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
-                    const uint32_t at = ss + (uint32_t)(lane * 16 + (t.n & 1) * 8);
+                    const uint32_t at = ss + (uint32_t)(lane * 16 + ((t.n * CG + rank) & 1) * 8);
                     const uint32_t to = ss + 1024u + (uint32_t)(lane * 16);
 #pragma unroll
                     for (uint32_t i = 0; i < 2; i++) {
@@ -694,7 +841,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         const int rw = warp - kRebuild0, grp = rw / 8;
         const int quarter = warp & 3, pc = (rw % 8) >> 2;
         const int row = 32 * quarter + lane;
-        Walk wk(pl, blockIdx.x);
+        Walk wk(pl, worker);
         Seg sg;
         Ring r, rt;
         bool ok = true;
@@ -732,19 +879,19 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t stg = base + p.stg_off;
         const size_t slot_f4 = (size_t)p.part_f4 * kTileN;   // float4s of a CTA's partial
-        Walk wk(pl, blockIdx.x);
+        Walk wk(pl, worker);
         Seg sg;
         Ring ra;
         while (wk.next(pl, p.kt, sg)) {
             const Tile t = locate(p, pl, sg.tile);
             const int cols = (t.rows + 15) & ~15;
-            const uint32_t lo = (uint32_t)(mma_n<SRC>(t.rows) / 2);   // split rows: first lo column
+            const uint32_t lo = (uint32_t)(mma_n<SRC, CG>(t.rows) / 2);   // split rows: first lo column
             const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
-            int last = blockIdx.x;
+            int last = worker;
             if (joins) last = unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
             bool good = true;
-            for (int b = blockIdx.x + 1; good && b <= last; b++)
-                good = wait_tag(p.flags + (size_t)b * 4 + warp, p.epoch, p.timeout, abort_flag);
+            for (int b = worker + 1; good && b <= last; b++)
+                good = wait_tag(p.flags + (size_t)(b * CG + rank) * 4 + warp, p.epoch, p.timeout, abort_flag);
             if (good) good = mbar_wait(accf + 8 * ra.i, ra.ph, p.timeout, abort_flag, 20000);
             if (any_of_epilogue(!good)) break;
             tc_fence_after();
@@ -780,7 +927,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                                  "l"(p.epoch)
                                  : "memory");
             } else {
-                const int64_t n0 = (int64_t)t.n * rows_a;
+                const int64_t n0 = ((int64_t)t.n * CG + rank) * rows_a;
                 for (int c0 = 0; c0 < cols; c0 += kChunk) {
                     // accumulator (and the other ranges' partial sums, in k order) -> staging
 #pragma unroll
@@ -789,8 +936,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                         if (c >= cols) break;
                         uint32_t v[16];
                         take(c, v);
-                        for (int b = blockIdx.x + 1; b <= last; b++) {
-                            const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)b * slot_f4 + row;
+                        for (int b = worker + 1; b <= last; b++) {
+                            const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row;
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
                                 const float4 x = __ldcg(src + (size_t)(c / 4 + i) * kTileN);
@@ -858,36 +1005,40 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
                 // the tags are cleared for a replay of this call
                 if (lane == 0)
-                    for (int b = blockIdx.x + 1; b <= last; b++) p.flags[(size_t)b * 4 + warp] = 0ull;
+                    for (int b = worker + 1; b <= last; b++) p.flags[(size_t)(b * CG + rank) * 4 + warp] = 0ull;
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce + 8 * ra.i);
+            if (lane == 0) {
+                if (CG == 2) release_at(in_first(acce + 8 * ra.i));
+                else mbar_arrive(acce + 8 * ra.i);
+            }
             ra.advance(p.nacc);
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();   // no CTA leaves while the other's MMAs or arrivals reach it
     if (*abort_flag && threadIdx.x == 0) raise_status(UW_ERR_TIMEOUT);
     if (warp == kMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        pair_dealloc<CG>(tmem, kTmemCols);
     }
 }
 
-template <int SRC>
+template <int SRC, int CG>
 __global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
     k_group(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
             const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<SRC>(tm_x, tm_w, tm_u, p);
+    group_body<SRC, CG>(tm_x, tm_w, tm_u, p);
 }
 
 // 22 warps: 16 K registers of a sub-partition over six of them allow 80.
 __global__ void __maxnreg__(80)
     k_group_rebuild(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<kGroupMx>(tm_x, tm_w, tm_u, p);
+    group_body<kGroupMx, 1>(tm_x, tm_w, tm_u, p);
 }
 
 // ---------------------------------------------------------------- rows before the product
@@ -896,7 +1047,7 @@ struct PrepParams {
     const int32_t* rows;      // NULL: slot s is row s
     const int32_t* offsets;
     int64_t x_rows, slots, K;
-    int E, MG, kt;
+    int E, MG, kt, round;
     uint32_t sf_bytes;        // scale bytes in front of a stage's rows
     int64_t chunk;
     uint8_t* out;
@@ -908,7 +1059,7 @@ constexpr int kPrepRows = 16;   // rows of a CTA: 2 a warp
 
 // Rows of split tiles: CTA (slot tile, 16 of its rows and 512 k); a warp takes
 // two rows, 16 values of each a lane, two lanes a block of 32.  Row r of a tile of n (rounded up
-// to 8) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
+// to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
 // swizzled rows; their scale bytes lie in front as tcgen05.cp reads them.
 // Bound by reading the rows and writing as many bytes.
 __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p) {
@@ -929,7 +1080,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p
     const int m = (int)blockIdx.x - cum[e];
     const int64_t s0 = (int64_t)begin[e] + (int64_t)m * p.MG;
     const int nrows = count[e] - m * p.MG < p.MG ? count[e] - m * p.MG : p.MG;
-    const int n8 = (nrows + 7) & ~7;
+    const int n8 = (nrows + p.round - 1) / p.round * p.round;   // as mma_n
     const int segs = (int)((p.K + kPrepK - 1) / kPrepK);
     const int r0 = (int)(blockIdx.y / segs) * kPrepRows + warp;
     const int64_t k = (int64_t)(blockIdx.y % segs) * kPrepK + 16 * lane;
@@ -1057,12 +1208,18 @@ int pick_tile_slots(int src, int64_t slots, int E) {
     return mg;
 }
 
+// Pairs of CTAs where tiles are large: a pair reads half of X per CTA, which
+// brings the bytes an SM has to take in below what L2 delivers (about 65 a
+// cycle) per MMA cycle.
+bool pick_pair(int src, int mg) { return src != kGroupMx && mg > 64; }
+
 constexpr size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How a call is cut up; the workspace holds partial sums, their tags, and the
 // prepared rows.
 struct Shape {
     int MG = 0, KB = 0, kt = 0, n_tiles = 0;
+    int CG = 1;               // CTAs of a worker
     int64_t m_tiles = 0;      // slot tiles at most
     bool gather = false;      // a gathered copy of BF16 rows
     uint32_t sf_b = 0;        // scale bytes of a stage's rows
@@ -1077,7 +1234,8 @@ Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, boo
     h.MG = pick_tile_slots(src, slots, E);
     h.KB = stage_k(src);
     h.kt = (int)((K + h.KB - 1) / h.KB);
-    const int rows_a = up ? kTileN / 2 : kTileN;
+    h.CG = pick_pair(src, h.MG) ? 2 : 1;
+    const int rows_a = h.CG * (up ? kTileN / 2 : kTileN);
     h.n_tiles = (int)((N + rows_a - 1) / rows_a);
     h.m_tiles = slots / h.MG + (E < slots ? E : slots);
     h.partial = (size_t)P * h.MG * kTileN * 4;
@@ -1099,17 +1257,20 @@ Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, boo
 int resolve(int src, int64_t K) { return src == kGroupMx && K % 128 == 0 ? kGroupMx8 : src; }
 
 template <typename K, typename... A>
-cudaError_t launch_after(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_after(K kern, dim3 grid, int cluster, int threads, size_t smem, cudaStream_t s, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1139,7 +1300,8 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.E = a.E;
     p.kt = h.kt;
     p.MG = MG;
-    p.box = MG < 64 ? MG : 64;
+    const int CG = h.CG;
+    p.box = MG / CG < 64 ? MG / CG : 64;
     p.up = a.up ? 1 : 0;
     p.n_tiles = h.n_tiles;
     p.out_f32 = a.out_f32;
@@ -1166,8 +1328,8 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.sf_b_bytes = h.sf_b;
     // (with `up`, split rows: a third part for the joined scales of both weights)
     p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up ? (src == kGroupMx8 ? 3 : 2) : 1) + p.sf_b_bytes);
-    p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1));
-    const uint32_t ctrl = 512, tab = (uint32_t)(3 * a.E + 1) * 4;
+    p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1) / CG);
+    const uint32_t ctrl = 1024, tab = (uint32_t)(3 * a.E + 1) * 4;
     const uint32_t fixed = 1024 + ctrl + kStage32 + ((tab + 15u) & ~15u);
     // tensor memory: accumulators, then rebuilt-A slots (32 columns) or scale columns
     p.acc_w = (uint32_t)(src == kGroupMx8 ? 2 * MG : MG);
@@ -1217,9 +1379,9 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     if (src == kGroupMx8) tx = tw;   // unused
 
     void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupParams) =
-        src == kGroupBf16   ? k_group<kGroupBf16>
-        : src == kGroupMxMx ? k_group<kGroupMxMx>
-        : src == kGroupMx8  ? k_group<kGroupMx8>
+        src == kGroupBf16   ? (CG == 2 ? k_group<kGroupBf16, 2> : k_group<kGroupBf16, 1>)
+        : src == kGroupMxMx ? (CG == 2 ? k_group<kGroupMxMx, 2> : k_group<kGroupMxMx, 1>)
+        : src == kGroupMx8  ? (CG == 2 ? k_group<kGroupMx8, 2> : k_group<kGroupMx8, 1>)
                             : k_group_rebuild;
     cudaError_t e = set_smem_attr((const void*)kern, (int)smem);
     if (e != cudaSuccess) return e;
@@ -1235,16 +1397,18 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
         q.E = a.E;
         q.MG = MG;
         q.kt = h.kt;
+        q.round = 8 * CG;
         q.sf_bytes = h.sf_b;
         q.chunk = h.chunk;
         q.out = prep;
         if (src == kGroupMx8)
-            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows))), kPrepThreads, tab, s, q);
+            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows))), 1, kPrepThreads, tab, s, q);
         else
-            e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), kPrepThreads, 0, s, q);
+            e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), 1, kPrepThreads, 0, s, q);
         if (e != cudaSuccess) return e;
     }
-    return launch_after(kern, dim3((unsigned)(max_tiles * h.kt < P ? max_tiles * h.kt : P)),
+    const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
+    return launch_after(kern, dim3((unsigned)(workers * CG)), CG,
                         src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 ? kThreadsMix : kThreadsPlain, smem, s, tx, tw, tu, p);
 }
 
