@@ -20,8 +20,8 @@
 //     contiguous range a CTA, so every SM reads until the end.  The CTA with a
 //     cut tile's first k steps reaches it last and adds the others' fp32
 //     partial rows in k order (from the workspace; deterministic);
-//   * warp roles: 0-3 epilogue, 4 TMA producer, 5 MMA issue (6: see kMix; 6-21:
-//     see kGroupMx);
+//   * warp roles: 0-7 epilogue, 8 TMA producer, 9 MMA issue (10: see kMix;
+//     12-19: see kGroupMx);
 //   * 4-bit weights with BF16 rows (kGroupMx8): the tensor cores take the codes
 //     and scales as they are, against 8-bit rows.  A BF16 value has 8
 //     significant bits, an e4m3 value 4: x = 2^s (hi + lo/16) with both in
@@ -33,7 +33,7 @@
 //     every tile in the order of its stages' shared memory, gathered, split
 //     and swizzled, so a stage's rows and scales are one bulk copy;
 //   * K an odd multiple of 64 (kGroupMx): the TMA's unpacking load wants rows
-//     of 128 codes, so warps 6-21 rebuild codes to BF16 in tensor memory, the
+//     of 128 codes, so warps 12-19 rebuild codes to BF16 in tensor memory, the
 //     MMA's A operand;
 //   * MXFP4 with MXFP4 rows (kGroupMxMx): block-scaled 4-bit MMA; the scale
 //     bytes go from shared to tensor memory (tcgen05.cp) in the order the
@@ -59,17 +59,18 @@ int group_status_take() { return unit_status_take(); }
 namespace {
 
 constexpr int kTileN = 128;            // weight rows of a tile
-constexpr int kProd = 4, kMma = 5, kRebuild0 = 6, kRebuildWarps = 16;
-constexpr int kThreadsPlain = 6 * 32;
-constexpr int kMix = 6;                // kGroupMx8: warp that joins the scales of two weights
-constexpr int kThreadsMix = 7 * 32;
+constexpr int kProd = 8, kMma = 9, kRebuild0 = 12, kRebuildWarps = 8;
+constexpr int kEpiWarps = 8;           // two per quarter of tensor memory's lanes
+constexpr int kMix = 10;               // kGroupMx8: warp that joins the scales of two weights
+constexpr int kThreadsPlain = 10 * 32;
+constexpr int kThreadsMix = 11 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
 constexpr int kMaxS = 12;              // stages
 constexpr int kMaxT = 8;               // rebuilt-A slots in tensor memory
 constexpr int kBand = 16;              // slot tiles of a band
 constexpr int kEpiBarId = 1;
-constexpr int kChunk = 32;             // slots the epilogue moves at a time
-constexpr uint32_t kStage32 = kChunk * kTileN * 4;   // epilogue staging: fp32 [32 slots][128 outputs]
+constexpr uint32_t kWarpStage = 1024;  // transpose buffer of an epilogue warp
+constexpr uint32_t kExchange = kEpiWarps * 2048;   // `up`: 16 slots x 32 rows of fp32 sums a warp
 constexpr uint32_t kTmemCols = 512;
 
 struct GroupParams {
@@ -95,7 +96,7 @@ struct GroupParams {
     int k_tiles;                            // scale tiles along k
     void* Y;
     float* partial;                         // [CTAs][MG/4][128] float4
-    unsigned long long* flags;              // [CTAs][4]: call tag once a warp's partial rows are out
+    unsigned long long* flags;              // [CTAs][8]: call tag once a warp's partial sums are out
     unsigned long long epoch;
     uint64_t timeout;
 };
@@ -190,13 +191,45 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int
     return t;
 }
 
-__device__ __forceinline__ uint16_t bf(float f) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(f);
-    return *reinterpret_cast<const uint16_t*>(&h);
-}
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Y[s0 + i, nw + lane] = v[i] for 16 slots (`valid` of them in the tile), by a
+// whole warp.  A lane holds one output of 16 slots; written so, a warp's
+// store would put 2 bytes a lane into 16 rows.  Instead slots go in pairs of
+// BF16 through 1 KB of shared memory and leave as 16-byte stores, four lanes a
+// slot.  Rows of N values that are not 16-byte aligned (N % 8) are stored value
+// by value, and so is fp32 (128 contiguous bytes a slot already).
+__device__ __forceinline__ void store16(const GroupParams& p, const uint32_t (&v)[16], int64_t s0, int valid, int64_t nw, int lane,
+                                        uint32_t stg) {
+    if (p.out_f32 || !p.y_vec) {
+        if (nw + lane >= p.N) return;
+        const int64_t at = s0 * p.N + nw + lane;
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            if (i < valid) {
+                if (p.out_f32) reinterpret_cast<float*>(p.Y)[at + i * p.N] = __uint_as_float(v[i]);
+                else reinterpret_cast<__nv_bfloat16*>(p.Y)[at + i * p.N] = __float2bfloat16_rn(__uint_as_float(v[i]));
+            }
+        return;
+    }
+    __syncwarp();   // the buffer's last readers are through
+#pragma unroll
+    for (int i = 0; i < 8; i++) sts32(stg + (uint32_t)(i * 128 + lane * 4), bf2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+    __syncwarp();
+    // lane: slots 2 (lane / 4) and the next, outputs 8 (lane % 4) ..
+    const int s = (lane >> 2) * 2, o = (lane & 3) * 8;
+    const uint4 a = lds128(stg + (uint32_t)((lane >> 2) * 128 + (lane & 3) * 32));
+    const uint4 b = lds128(stg + (uint32_t)((lane >> 2) * 128 + (lane & 3) * 32 + 16));
+    if (nw + o >= p.N) return;
+    uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + (s0 + s) * p.N + nw + o;
+    if (s < valid)
+        *reinterpret_cast<uint4*>(y) = make_uint4(prmt(a.x, a.y, 0x5410u), prmt(a.z, a.w, 0x5410u), prmt(b.x, b.y, 0x5410u), prmt(b.z, b.w, 0x5410u));
+    if (s + 1 < valid)
+        *reinterpret_cast<uint4*>(y + p.N) =
+            make_uint4(prmt(a.x, a.y, 0x7632u), prmt(a.z, a.w, 0x7632u), prmt(b.x, b.y, 0x7632u), prmt(b.z, b.w, 0x7632u));
 }
 
 __device__ __forceinline__ bool any_of_epilogue(bool pred) {
@@ -207,7 +240,7 @@ __device__ __forceinline__ bool any_of_epilogue(bool pred) {
         "bar.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(res)
-        : "r"((uint32_t)pred), "n"(kEpiBarId), "n"(4 * 32)
+        : "r"((uint32_t)pred), "n"(kEpiBarId), "n"(kEpiWarps * 32)
         : "memory");
     return res != 0;
 }
@@ -590,12 +623,12 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             mbar_init(mixed + 8 * s, 1);
         }
         for (int t = 0; t < p.T; t++) {
-            mbar_init(recon + 8 * t, kRebuildWarps / 2);
+            mbar_init(recon + 8 * t, kRebuildWarps);
             mbar_init(tfree + 8 * t, 1);
         }
         for (int a = 0; a < 2; a++) {
             mbar_init(accf + 8 * a, 1);
-            mbar_init(acce + 8 * a, 4 * CG);
+            mbar_init(acce + 8 * a, kEpiWarps * CG);
         }
         mbar_init(fin, 1);
         *abort_flag = 0;
@@ -730,7 +763,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         uint32_t ph = 0, fb = full, lo = lo0, sf = tmem + p.sf_col0;
         bool ok = true;
         while (ok && wk.next(pl, p.kt, sg)) {
-            const int nN = mma_n<SRC, CG>(locate(p, pl, sg.tile).rows);
+            const Tile t = locate(p, pl, sg.tile);
+            const int nN = mma_n<SRC, CG>(t.rows);
             const uint32_t idesc = SRC == kGroupMx8    ? idesc_mx8(CG, nN, 0)
                                    : SRC == kGroupMxMx ? idesc_mx(CG, nN, 0)
                                                        : mma_idesc_bf16(CG * kTileN, nN);
@@ -748,6 +782,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                     // scales of the stage, 4 columns per 512 bytes: weights, then rows
                     const uint32_t ss = lo + (p.off_s >> 4), sb = lo + lo_b - (p.sf_b_bytes >> 4);
                     const uint32_t sfb = sf + (SRC == kGroupMxMx ? 8u : 4u);
+                    // a tile of 192 slots may start in the middle of a scale tile: two columns on
+                    const uint32_t sfx = SRC == kGroupMxMx ? sfb + (uint32_t)(t.s0 % kMxTileRows) / 32u : sfb;
                     if (SRC == kGroupMxMx) {
                         const uint32_t nb = p.sf_b_bytes / kMxTileBytes;
 #pragma unroll
@@ -759,14 +795,14 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
 #pragma unroll
                         for (uint32_t j = 0; j < 4; j++, more = 1)
                             tc_mma_mx<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
-                                      sf + 4u * (j >> 1), sfb + 4u * nb * (j >> 1), more);
+                                      sf + 4u * (j >> 1), sfx + 4u * nb * (j >> 1), more);
                     } else {
                         tc_copy_scales<CG>(sf, p.up ? ss + 64u : ss);
                         tc_copy_scales<CG>(sfb, sb);
                         if (p.sf_b_bytes > 512u) tc_copy_scales<CG>(sfb + 4u, sb + 32u);
 #pragma unroll
                         for (uint32_t j = 0; j < 4; j++, more = 1)
-                            tc_mma_mx8<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + j * ((1u << 4) | (1u << 29)), sf, sfb,
+                            tc_mma_mx8<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + j * ((1u << 4) | (1u << 29)), sf, sfx,
                                        more);
                     }
                     sf += p.sf_slot;
@@ -834,12 +870,9 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         }
     } else if (kRe && warp >= kRebuild0) {
         // ------------------------------------------------------------ rebuild
-        // Warp w owns tensor-memory lanes (weight rows) 32 (w % 4) ..; two groups
-        // of eight take alternate stages, two warps of a quarter one piece of
-        // 32 k each.  S and T are even, so a group meets the same slots in
-        // every round and sees all their phases in turn.
-        const int rw = warp - kRebuild0, grp = rw / 8;
-        const int quarter = warp & 3, pc = (rw % 8) >> 2;
+        // Warp w owns tensor-memory lanes (weight rows) 32 (w % 4) ..; the two
+        // warps of a quarter take one piece of 32 k each.
+        const int quarter = warp & 3, pc = (warp - kRebuild0) >> 2;
         const int row = 32 * quarter + lane;
         Walk wk(pl, worker);
         Seg sg;
@@ -856,7 +889,6 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             }
             so += (uint32_t)(lane * 16 + sq * 4);
             for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S), rt.advance(p.T)) {
-                if ((rt.i & 1) != grp) continue;
                 if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (!mbar_wait(tfree + 8 * rt.i, rt.ph ^ 1u, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
@@ -873,11 +905,14 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 if (lane == 0) mbar_arrive(recon + 8 * rt.i);
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < kEpiWarps) {
         // ------------------------------------------------------------ epilogue
-        const int row = warp * 32 + lane;
-        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t stg = base + p.stg_off;
+        // Warps q and q + 4 share the tile's rows 32 q ..; of every 32 slots the
+        // first takes 16 and the second 16 (with `up`: of every 64, 32 each).
+        const int quarter = warp & 3, set = warp >> 2;
+        const int row = quarter * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t stg = base + p.stg_off + (uint32_t)warp * kWarpStage, xch = base + p.stg_off + kEpiWarps * kWarpStage;
         const size_t slot_f4 = (size_t)p.part_f4 * kTileN;   // float4s of a CTA's partial
         Walk wk(pl, worker);
         Seg sg;
@@ -891,7 +926,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             if (joins) last = unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
             bool good = true;
             for (int b = worker + 1; good && b <= last; b++)
-                good = wait_tag(p.flags + (size_t)(b * CG + rank) * 4 + warp, p.epoch, p.timeout, abort_flag);
+                good = wait_tag(p.flags + (size_t)(b * CG + rank) * kEpiWarps + warp, p.epoch, p.timeout, abort_flag);
             if (good) good = mbar_wait(accf + 8 * ra.i, ra.ph, p.timeout, abort_flag, 20000);
             if (any_of_epilogue(!good)) break;
             tc_fence_after();
@@ -912,6 +947,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             if (publish) {
                 float4* dst = reinterpret_cast<float4*>(p.partial) + (size_t)blockIdx.x * slot_f4 + row;
                 for (int c = 0; c < cols; c += 16) {
+                    if ((c >> (p.up ? 5 : 4) & 1) != set) continue;
                     uint32_t v[16];
                     take(c, v);
 #pragma unroll
@@ -923,89 +959,70 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 __threadfence();
                 __syncwarp();
                 if (lane == 0)
-                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)blockIdx.x * 4 + warp),
+                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)blockIdx.x * kEpiWarps + warp),
                                  "l"(p.epoch)
                                  : "memory");
             } else {
-                const int64_t n0 = ((int64_t)t.n * CG + rank) * rows_a;
-                for (int c0 = 0; c0 < cols; c0 += kChunk) {
-                    // accumulator (and the other ranges' partial sums, in k order) -> staging
+                // 16 slots of the finished sum: the accumulator plus the other ranges' partial sums, in k order
+                auto sum = [&](int c, uint32_t (&v)[16]) {
+                    take(c, v);
+                    for (int b = worker + 1; b <= last; b++) {
+                        const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row;
 #pragma unroll
-                    for (int hh = 0; hh < 2; hh++) {
-                        const int c = c0 + 16 * hh;
-                        if (c >= cols) break;
-                        uint32_t v[16];
-                        take(c, v);
-                        for (int b = worker + 1; b <= last; b++) {
-                            const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row;
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const float4 x = __ldcg(src + (size_t)(c / 4 + i) * kTileN);
-                                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + x.x);
-                                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + x.y);
-                                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + x.z);
-                                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + x.w);
-                            }
+                        for (int i = 0; i < 4; i++) {
+                            const float4 x = __ldcg(src + (size_t)(c / 4 + i) * kTileN);
+                            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + x.x);
+                            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + x.y);
+                            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + x.z);
+                            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + x.w);
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; i++) sts32(stg + (uint32_t)((16 * hh + i) * kTileN + row) * 4u, v[i]);
                     }
-                    named_bar_sync(kEpiBarId, 128);
-                    // staging -> Y, 8 outputs a thread
-                    const int per = rows_a / 8, cnt = t.rows - c0 < kChunk ? t.rows - c0 : kChunk;
-                    for (int i = threadIdx.x; i < cnt * per; i += 128) {
-                        const int s = i / per, o = (i % per) * 8;
-                        float v[8];
+                };
+                // first output of this warp: 32 rows of W, or of W and `up` each (warps w and w + 2)
+                const int64_t nw = ((int64_t)t.n * CG + rank) * rows_a + 32 * (p.up ? quarter & 1 : quarter);
+                if (!p.up) {
+                    for (int c = 16 * set; c < cols; c += 32) {
+                        uint32_t v[16];
+                        sum(c, v);
+                        store16(p, v, t.s0 + c, t.rows - c, nw, lane, stg);
+                    }
+                } else {
+                    // Quarter q holds rows of W, quarter q + 2 the same rows of `up`: of every 32 slots the first
+                    // computes 16 and gets their `up` sums, the second the other 16 and gets their W sums.
+                    const uint32_t mine = xch + (uint32_t)warp * 2048u + (uint32_t)lane * 4u;
+                    const uint32_t theirs = xch + (uint32_t)(warp ^ 2) * 2048u + (uint32_t)lane * 4u;
+                    const bool first = quarter < 2;
+                    const int bar = kEpiBarId + 1 + (quarter & 1) + 2 * set;
+                    for (int c0 = 32 * set; c0 < cols; c0 += 64) {
+                        uint32_t keep[16], give[16];
+                        const int ck = c0 + (first ? 0 : 16), cg = c0 + (first ? 16 : 0);
+                        if (cg < cols) {
+                            sum(cg, give);
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const uint4 x = lds128(stg + (uint32_t)(s * kTileN + o + 4 * h) * 4u);
-                            v[4 * h] = __uint_as_float(x.x);
-                            v[4 * h + 1] = __uint_as_float(x.y);
-                            v[4 * h + 2] = __uint_as_float(x.z);
-                            v[4 * h + 3] = __uint_as_float(x.w);
+                            for (int i = 0; i < 16; i++) sts32(mine + (uint32_t)(128 * i), give[i]);
                         }
-                        if (p.up) {
+                        if (ck < cols) sum(ck, keep);
+                        named_bar_sync(bar, 64);
+                        if (ck < cols) {
+                            const int valid = t.rows - ck;
 #pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                const uint4 x = lds128(stg + (uint32_t)(s * kTileN + 64 + o + 4 * h) * 4u);
-                                const float u[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
-                                                    __uint_as_float(x.w)};
+                            for (int i0 = 0; i0 < 16; i0 += 4) {
+                                if (i0 >= valid) break;
 #pragma unroll
-                                for (int j = 0; j < 4; j++) {
-                                    const float g = v[4 * h + j];
-                                    v[4 * h + j] = g / (1.0f + __expf(-g)) * u[j];
+                                for (int i = i0; i < i0 + 4; i++) {
+                                    const float o = __uint_as_float(lds32(theirs + (uint32_t)(128 * i)));
+                                    const float g = first ? __uint_as_float(keep[i]) : o, u = first ? o : __uint_as_float(keep[i]);
+                                    keep[i] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * u);
                                 }
                             }
+                            store16(p, keep, t.s0 + ck, valid, nw, lane, stg);
                         }
-                        const int64_t n = n0 + o;
-                        const int64_t at = (t.s0 + c0 + s) * p.N + n;
-                        if (p.out_f32) {
-                            float* y = reinterpret_cast<float*>(p.Y) + at;
-                            if (p.y_vec && n + 8 <= p.N) {
-                                reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; j++)
-                                    if (n + j < p.N) y[j] = v[j];
-                            }
-                        } else {
-                            uint16_t* y = reinterpret_cast<uint16_t*>(p.Y) + at;
-                            if (p.y_vec && n + 8 <= p.N) {
-                                *reinterpret_cast<uint4*>(y) =
-                                    make_uint4(bf2(v[0], v[1]), bf2(v[2], v[3]), bf2(v[4], v[5]), bf2(v[6], v[7]));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; j++)
-                                    if (n + j < p.N) y[j] = bf(v[j]);
-                            }
-                        }
+                        if (c0 + 64 < cols) named_bar_sync(bar, 64);   // the sums have been read
                     }
-                    named_bar_sync(kEpiBarId, 128);
                 }
                 // the tags are cleared for a replay of this call
                 if (lane == 0)
-                    for (int b = worker + 1; b <= last; b++) p.flags[(size_t)(b * CG + rank) * 4 + warp] = 0ull;
+                    for (int b = worker + 1; b <= last; b++) p.flags[(size_t)(b * CG + rank) * kEpiWarps + warp] = 0ull;
             }
             tc_fence_before();
             __syncwarp();
@@ -1034,8 +1051,7 @@ __global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain
     group_body<SRC, CG>(tm_x, tm_w, tm_u, p);
 }
 
-// 22 warps: 16 K registers of a sub-partition over six of them allow 80.
-__global__ void __maxnreg__(80)
+__global__ void __launch_bounds__(kThreadsRebuild, 1)
     k_group_rebuild(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
     group_body<kGroupMx, 1>(tm_x, tm_w, tm_u, p);
@@ -1197,7 +1213,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_gather(const PrepParams 
 
 // Slots of a tile: twice the mean group (groups are uneven), a power of two
 // from 16 up.  At most 256; 112 split rows (two accumulators and the scales
-// fit tensor memory).  Block-scaled products keep 128-slot scale tiles whole.
+// fit tensor memory).  Block-scaled products take 128 or 192: two accumulators
+// and the scales fit, and tiles start at half a scale tile at worst.
 int pick_tile_slots(int src, int64_t slots, int E) {
     const int64_t groups = E < slots ? E : slots;
     const int64_t mean = (slots + groups - 1) / groups;
@@ -1205,6 +1222,7 @@ int pick_tile_slots(int src, int64_t slots, int E) {
     int mg = src == kGroupMxMx ? 128 : 16;
     while (mg < 256 && mg < want) mg *= 2;
     if (src == kGroupMx8 && mg > 64) mg = 112;
+    if (src == kGroupMxMx && mg > 128) mg = 192;
     return mg;
 }
 
@@ -1239,13 +1257,13 @@ Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, boo
     h.n_tiles = (int)((N + rows_a - 1) / rows_a);
     h.m_tiles = slots / h.MG + (E < slots ? E : slots);
     h.partial = (size_t)P * h.MG * kTileN * 4;
-    h.flags = al256((size_t)P * 4 * 8);
+    h.flags = al256((size_t)P * kEpiWarps * 8);
     if (src == kGroupMx8) {
         h.sf_b = 512u * (uint32_t)((2 * h.MG + 127) / 128);
         h.chunk = (int64_t)h.sf_b + 2 * h.MG * 128;
         h.prep = al256((size_t)h.m_tiles * h.kt * h.chunk);
     } else if (src == kGroupMxMx) {
-        h.sf_b = (uint32_t)(h.MG / kMxTileRows) * kMxTileBytes;
+        h.sf_b = (uint32_t)mx_row_tiles(h.MG) * kMxTileBytes;
     } else if (rows && h.MG > 32) {
         h.gather = true;
         h.prep = al256((size_t)slots * (size_t)K * 2);
@@ -1301,7 +1319,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.kt = h.kt;
     p.MG = MG;
     const int CG = h.CG;
-    p.box = MG / CG < 64 ? MG / CG : 64;
+    p.box = MG / CG % 64 ? MG / CG : 64;   // divides MG / CG: boxes never pass the rows set aside
     p.up = a.up ? 1 : 0;
     p.n_tiles = h.n_tiles;
     p.out_f32 = a.out_f32;
@@ -1330,11 +1348,12 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up ? (src == kGroupMx8 ? 3 : 2) : 1) + p.sf_b_bytes);
     p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1) / CG);
     const uint32_t ctrl = 1024, tab = (uint32_t)(3 * a.E + 1) * 4;
-    const uint32_t fixed = 1024 + ctrl + kStage32 + ((tab + 15u) & ~15u);
+    const uint32_t epi = kEpiWarps * kWarpStage + (p.up ? kExchange : 0);
+    const uint32_t fixed = 1024 + ctrl + epi + ((tab + 15u) & ~15u);
     // tensor memory: accumulators, then rebuilt-A slots (32 columns) or scale columns
     p.acc_w = (uint32_t)(src == kGroupMx8 ? 2 * MG : MG);
-    p.sf_slot = src == kGroupMxMx ? 8u + 8u * (uint32_t)(MG / kMxTileRows) : src == kGroupMx8 ? 4u + h.sf_b / 128u : 0u;
-    p.nacc = src == kGroupBf16 || src == kGroupMx8 || 2 * MG <= 256 ? 2 : 1;
+    p.sf_slot = src == kGroupMxMx ? 8u + 8u * (uint32_t)mx_row_tiles(MG) : src == kGroupMx8 ? 4u + h.sf_b / 128u : 0u;
+    p.nacc = src == kGroupMx && MG > 128 ? 1 : 2;   // (rebuilt-A slots take half of tensor memory)
     const uint32_t acc_cols = (uint32_t)p.nacc * p.acc_w;
     int S = (int)((227 * 1024 - fixed) / p.stage_bytes);
     if (S > kMaxS) S = kMaxS;
@@ -1342,15 +1361,13 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     if (src == kGroupMx) {
         p.T = (int)((kTmemCols - acc_cols) / 32u);
         if (p.T > kMaxT) p.T = kMaxT;
-        S &= ~1;   // two rebuild groups: even rings
-        p.T &= ~1;
     }
     if (S < 2 || (src == kGroupMx && p.T < 2)) { *st = UW_ERR_UNSUPPORTED; return cudaSuccess; }
     p.S = S;
     p.a_col0 = p.sf_col0 = acc_cols;
     p.ctrl_off = (uint32_t)S * p.stage_bytes;
     p.stg_off = p.ctrl_off + ctrl;
-    p.tab_off = p.stg_off + kStage32;
+    p.tab_off = p.stg_off + epi;
     const size_t smem = (size_t)S * p.stage_bytes + fixed;
 
     CUtensorMap tx{}, tw{}, tu{};
