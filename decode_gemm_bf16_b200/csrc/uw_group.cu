@@ -15,11 +15,11 @@
 //   * tiles are listed on the device from the offsets: expert by expert, in
 //     bands of 16 slot tiles with the slot tile fastest, so that CTAs working
 //     at the same time share weight tiles and slot tiles in L2;
-//   * one persistent CTA per SM.  All full rounds of whole tiles but the last
-//     are dealt out one tile a CTA; the rest is cut into equal k ranges, one
-//     contiguous range a CTA, so every SM reads until the end.  The CTA with a
-//     cut tile's first k steps reaches it last and adds the others' fp32
-//     partial rows in k order (from the workspace; deterministic);
+//   * one persistent CTA per SM, in pairs (cta_group::2: one MMA over 256 weight
+//     rows) where tiles are large.  Full rounds of whole tiles are dealt out one
+//     a worker; what is left over is cut along k (see Plan).  The worker with a
+//     cut tile's first k steps adds the others' fp32 partial sums in k order
+//     (from the workspace; deterministic);
 //   * warp roles: 0-7 epilogue, 8 TMA producer, 9 MMA issue (10: see kMix;
 //     12-19: see kGroupMx);
 //   * 4-bit weights with BF16 rows (kGroupMx8): the tensor cores take the codes
@@ -84,6 +84,8 @@ struct GroupParams {
     uint32_t sf_a_bytes, sf_b_bytes;        // scale bytes of a stage: weights (one matrix), X
     uint32_t sf_slot;                       // scale columns of a stage
     uint32_t a_col0, sf_col0;
+    int step;                               // tiles of a group hold a multiple of this many slots
+    int parts;                              // cut tiles in equal parts (see Plan)
     int early;                              // a preparing kernel of this call ran just before
     const uint8_t* prep;                    // kGroupMx8: [slot tiles][kt][scales, rows]
     int64_t prep_chunk;                     // bytes of one stage of one tile there
@@ -112,21 +114,37 @@ struct Ring {
     }
 };
 
-// The tile list as every role sees it (shared memory) and a CTA's share of it.
+// The tile list as every role sees it (shared memory) and how it is shared
+// out.  Whole tiles are dealt out in rounds, one a worker (a CTA or a pair).
+// The rest is cut along k, either
+//   * in equal contiguous ranges of k steps, one a worker (`ps` workers), or
+//   * (parts > 0) every one of the last `rest` tiles in `parts` equal parts,
+//     worker part * rest + i taking a part of tile i.
 struct Plan {
     const int32_t* cum;      // [E + 1] tiles before each expert
     const int32_t* begin;    // [E] first slot
     const int32_t* count;    // [E] slots
     int64_t tiles, whole;    // tiles; tiles dealt out whole (the first ones)
-    int64_t units;           // k steps of the cut tiles
-    int ps;                  // of the P workers (CTAs or pairs), those that share them
+    int64_t units;           // k steps of the cut tiles (contiguous ranges)
+    int ps;                  // of the P workers, those that share them
     int P;
+    int parts, rest;
 };
 
 struct Seg {
     int64_t tile;
     int kt0, kt1;
 };
+
+// Slots of a tile of a group of c: the group is cut into as few tiles of at
+// most MG slots as it takes, all of one size but the last (a multiple of
+// `step`, so never more than MG).  Even tiles keep the workers of a round in
+// step; a short last tile would let its worker run ahead (8 uneven experts,
+// 4096 x 14336 in BF16: XXX us -> XXX us).
+__device__ __forceinline__ int tile_slots(int c, int MG, int step) {
+    const int mt = (c + MG - 1) / MG, even = (c + mt - 1) / mt;
+    return (even + step - 1) / step * step;
+}
 
 struct Tile {
     int e, n, rows;          // expert, weight tile, slots of the tile
@@ -138,9 +156,11 @@ struct Tile {
 __device__ __forceinline__ int64_t unit_begin(int64_t b, const Plan& pl) { return b * pl.units / pl.ps; }
 __device__ __forceinline__ int unit_owner(int64_t u, const Plan& pl) { return (int)(((u + 1) * pl.ps - 1) / pl.units); }
 
-// A worker's segments: its range of the cut tiles, then its whole tiles.
+// A worker's segments: its range or part of the cut tiles first (joining them
+// then overlaps the whole tiles), then its whole tiles.
 struct Walk {
     int64_t u, ue, t;
+    int part, own;
     __device__ __forceinline__ Walk(const Plan& pl, int b) {
         u = ue = 0;
         if (b < pl.ps) {
@@ -148,6 +168,8 @@ struct Walk {
             ue = unit_begin(b + 1, pl);
         }
         t = b;
+        part = pl.parts && b < pl.parts * pl.rest ? b / pl.rest : -1;
+        own = part > 0 ? b - part * pl.rest : b;
     }
     __device__ __forceinline__ bool next(const Plan& pl, int kt, Seg& s) {
         if (u < ue) {
@@ -156,6 +178,13 @@ struct Walk {
             const int64_t left = ue - u;
             s.kt1 = left < kt - s.kt0 ? s.kt0 + (int)left : kt;
             u += s.kt1 - s.kt0;
+            return true;
+        }
+        if (part >= 0) {
+            s.tile = pl.whole + own;
+            s.kt0 = part * kt / pl.parts;
+            s.kt1 = (part + 1) * kt / pl.parts;
+            part = -1;
             return true;
         }
         if (t < pl.whole) {
@@ -185,9 +214,10 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int
     t.e = lo;
     t.n = l / nb;
     const int m = band * kBand + l % nb;
-    t.s0 = (int64_t)pl.begin[lo] + (int64_t)m * p.MG;
+    const int each = tile_slots(c, p.MG, p.step);
+    t.s0 = (int64_t)pl.begin[lo] + (int64_t)m * each;
     t.m = pl.cum[lo] / p.n_tiles + m;
-    t.rows = c - m * p.MG < p.MG ? c - m * p.MG : p.MG;
+    t.rows = c - m * each < each ? c - m * each : each;
     return t;
 }
 
@@ -657,13 +687,24 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     pl.count = count;
     pl.tiles = cum[p.E];
     {
-        const int64_t P = gridDim.x / CG, rounds = pl.tiles / P;
+        const int64_t P = gridDim.x / CG, rounds = pl.tiles / P, rest = pl.tiles % P;
         pl.P = (int)P;
-        pl.whole = pl.tiles % P == 0 ? pl.tiles : rounds > 1 ? (rounds - 1) * P : 0;
-        pl.units = (pl.tiles - pl.whole) * p.kt;
-        // a range shorter than two k steps costs more to join than it saves
-        const int64_t most = (pl.units + 1) / 2;
-        pl.ps = (int)(P < most ? P : most);
+        pl.units = pl.ps = pl.parts = pl.rest = 0;
+        pl.whole = pl.tiles;
+        if (p.parts) {
+            const int64_t most = rest ? P / rest : 0, parts = most < p.kt / 2 ? most : p.kt / 2;   // two k steps at least
+            if (parts > 1) {
+                pl.parts = (int)parts;
+                pl.rest = (int)rest;
+                pl.whole = pl.tiles - rest;
+            }
+        } else if (rest) {
+            pl.whole = rounds > 1 ? (rounds - 1) * P : 0;
+            pl.units = (pl.tiles - pl.whole) * p.kt;
+            // a range shorter than two k steps costs more to join than it saves
+            const int64_t most = (pl.units + 1) / 2;
+            pl.ps = (int)(P < most ? P : most);
+        }
     }
     const int rows_a = p.up ? kTileN / 2 : kTileN;   // outputs of a tile
 
@@ -922,10 +963,12 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             const int cols = (t.rows + 15) & ~15;
             const uint32_t lo = (uint32_t)(mma_n<SRC, CG>(t.rows) / 2);   // split rows: first lo column
             const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
+            // the tile's other ranges, in k order: workers worker + stride, ... up to `last`
+            const int stride = pl.parts ? pl.rest : 1;
             int last = worker;
-            if (joins) last = unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
+            if (joins) last = pl.parts ? worker + (pl.parts - 1) * stride : unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
             bool good = true;
-            for (int b = worker + 1; good && b <= last; b++)
+            for (int b = worker + stride; good && b <= last; b += stride)
                 good = wait_tag(p.flags + (size_t)(b * CG + rank) * kEpiWarps + warp, p.epoch, p.timeout, abort_flag);
             if (good) good = mbar_wait(accf + 8 * ra.i, ra.ph, p.timeout, abort_flag, 20000);
             if (any_of_epilogue(!good)) break;
@@ -966,7 +1009,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 // 16 slots of the finished sum: the accumulator plus the other ranges' partial sums, in k order
                 auto sum = [&](int c, uint32_t (&v)[16]) {
                     take(c, v);
-                    for (int b = worker + 1; b <= last; b++) {
+                    for (int b = worker + stride; b <= last; b += stride) {
                         const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row;
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
@@ -1022,7 +1065,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
                 // the tags are cleared for a replay of this call
                 if (lane == 0)
-                    for (int b = worker + 1; b <= last; b++) p.flags[(size_t)(b * CG + rank) * kEpiWarps + warp] = 0ull;
+                    for (int b = worker + stride; b <= last; b += stride) p.flags[(size_t)(b * CG + rank) * kEpiWarps + warp] = 0ull;
             }
             tc_fence_before();
             __syncwarp();
@@ -1063,7 +1106,7 @@ struct PrepParams {
     const int32_t* rows;      // NULL: slot s is row s
     const int32_t* offsets;
     int64_t x_rows, slots, K;
-    int E, MG, kt, round;
+    int E, MG, kt, round, step;
     uint32_t sf_bytes;        // scale bytes in front of a stage's rows
     int64_t chunk;
     uint8_t* out;
@@ -1094,8 +1137,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p
         if (cum[mid] <= (int)blockIdx.x) e = mid; else hi = mid;
     }
     const int m = (int)blockIdx.x - cum[e];
-    const int64_t s0 = (int64_t)begin[e] + (int64_t)m * p.MG;
-    const int nrows = count[e] - m * p.MG < p.MG ? count[e] - m * p.MG : p.MG;
+    const int each = tile_slots(count[e], p.MG, p.step);
+    const int64_t s0 = (int64_t)begin[e] + (int64_t)m * each;
+    const int nrows = count[e] - m * each < each ? count[e] - m * each : each;
     const int n8 = (nrows + p.round - 1) / p.round * p.round;   // as mma_n
     const int segs = (int)((p.K + kPrepK - 1) / kPrepK);
     const int r0 = (int)(blockIdx.y / segs) * kPrepRows + warp;
@@ -1231,6 +1275,13 @@ int pick_tile_slots(int src, int64_t slots, int E) {
 // cycle) per MMA cycle.
 bool pick_pair(int src, int mg) { return src != kGroupMx && mg > 64; }
 
+// How tiles that fill no round are cut.  Contiguous ranges keep every SM
+// reading to the end, which small tiles (bound by reading weights) need.
+// With pairs the workers of a round share weight and slot tiles in L2 because
+// they walk k together; ranges that start anywhere lose that (8 experts of
+// 1024 rows, 4096 x 14336 in BF16: 728 us with ranges, XXX with parts).
+bool pick_parts(int CG) { return CG == 2; }
+
 constexpr size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How a call is cut up; the workspace holds partial sums, their tags, and the
@@ -1331,6 +1382,9 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.w_row_tiles = mx_row_tiles(a.N);
     p.k_tiles = (int)mx_k_tiles(a.K);
     p.early = src == kGroupMx8 || h.gather;
+    p.parts = pick_parts(CG);
+    // what the MMA's N rounds a tile to; half a scale tile for 4-bit rows
+    p.step = src == kGroupMx8 ? 8 * CG : src == kGroupMxMx ? 64 : 16 * CG;
     p.prep = prep;
     p.prep_chunk = h.chunk;
     p.part_f4 = MG / 4;
@@ -1415,6 +1469,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
         q.MG = MG;
         q.kt = h.kt;
         q.round = 8 * CG;
+        q.step = p.step;
         q.sf_bytes = h.sf_b;
         q.chunk = h.chunk;
         q.out = prep;
