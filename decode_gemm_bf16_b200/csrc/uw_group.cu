@@ -73,6 +73,14 @@ constexpr uint32_t kWarpStage = 1024;  // transpose buffer of an epilogue warp
 constexpr uint32_t kExchange = kEpiWarps * 2048;   // `up`: 16 slots x 32 rows of fp32 sums a warp
 constexpr uint32_t kTmemCols = 512;
 
+// Tensor maps of a call (unused ones are left empty).
+struct Maps {
+    CUtensorMap x;        // rows of X (or, split rows, 16 prepared rows a box)
+    CUtensorMap w, u;     // weights
+    CUtensorMap sw;       // W's scale tiles, 512 bytes a row (pairs)
+    CUtensorMap sx;       // X's (pairs; split rows: the scales in front of the prepared rows)
+};
+
 struct GroupParams {
     int64_t x_rows, slots, N;
     const int32_t* rows;
@@ -476,9 +484,9 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
     return a;
 }
-// arrive_at orders nothing: it passes on that copies have landed, which the
-// tensor cores then read where they are.  (With .release.cluster a stage took
-// 1600 cycles instead of 560.)
+// arrive_at itself orders nothing: the scales that kMix wrote are ordered by
+// its fence to the proxy that reads them.  (A release at cluster scope costs
+// about 1600 cycles, three stages' time.)
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -495,6 +503,20 @@ __device__ __forceinline__ bool test_cluster(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+// A box into this CTA's shared memory, counted on the barrier of the pair's
+// first CTA (`bar`: its cluster address).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if (CG == 1) tma_load_2d(dst, map, x, y, bar);
+    else tma_load_pair(dst, map, x, y, bar);
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -528,6 +550,8 @@ __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_
 
 // What the producer thread loads for the stages of one tile, from k step kt on:
 // everything that changes from stage to stage is advanced, not computed anew.
+// In a pair every load counts on the first CTA's barrier, which expects the
+// bytes of both; only the scales that kMix joins have a barrier in each CTA.
 template <int SRC, int CG>
 struct Feed {
     static constexpr int KB = stage_k(SRC);
@@ -536,96 +560,127 @@ struct Feed {
     int ax, w0, w1;              // column and rows of the weight boxes
     const uint8_t* s0;           // scales of the stage's weights (and of `up`)
     const uint8_t* s1;
+    int sy;                      // ... their half tile (pairs)
     int half;                    // kGroupMx: a scale half tile (128 k) serves two stages
     const uint8_t* x0;           // split rows, or the scales of 128 rows of X (and of the next 128)
     const uint8_t* x1;
+    int xy0, xy1;                // ... their row or half tile (pairs)
     int bx, y, boxes, gathers;
-    uint32_t x_bytes, x_at, tx;  // X: bytes, and where this CTA's half starts
+    uint32_t x_bytes, tx;
 
-    __device__ __forceinline__ Feed(const GroupParams& p, const CUtensorMap& tm_w, const CUtensorMap& tm_u, const Tile& t, int kt,
-                                    int rank) {
+    __device__ __forceinline__ Feed(const GroupParams& p, const Maps& m, const Tile& t, int kt, int rank) {
         const int n0 = (t.n * CG + rank) * (p.up ? kTileN / 2 : kTileN), nN = mma_n<SRC, CG>(t.rows) / CG;
         w0 = t.e * (int)p.N + n0;   // E N is below 2^31
         w1 = p.up ? w0 : w0 + kTileN / 2;
-        second = p.up ? &tm_u : &tm_w;
+        second = p.up ? &m.u : &m.w;
         // codes that the TMA unpacks count as elements of a box, packed ones as bytes
         ax = kt * (SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2);
         bx = kt * (SRC == kGroupMxMx ? KB / 2 : KB);
         y = (int)t.s0 + rank * nN;
-        x_at = p.sf_b_bytes + (uint32_t)(rank * nN) * 128u;
         boxes = (nN + p.box - 1) / p.box;
-        gathers = p.rows ? (t.rows + 3) / 4 : 0;
-        x_bytes = SRC == kGroupMx8 ? (uint32_t)nN * 128u : p.rows ? (uint32_t)gathers * 512u : (uint32_t)(boxes * p.box) * 128u;
+        gathers = CG == 1 && p.rows ? (t.rows + 3) / 4 : 0;
+        x_bytes = SRC == kGroupMx8 && CG == 1 ? (uint32_t)nN * 128u : gathers ? (uint32_t)gathers * 512u : (uint32_t)(boxes * p.box) * 128u;
         // the unpacking load counts the packed bytes of its rows
-        tx = (uint32_t)kTileN * (SRC == kGroupMx8 ? 64u : kARow) + p.sf_a_bytes * (p.up ? 2u : 1u) + p.sf_b_bytes + x_bytes;
+        tx = (uint32_t)kTileN * (SRC == kGroupMx8 ? 64u : kARow) + p.sf_b_bytes + x_bytes;
+        if (!joined(p)) tx += p.sf_a_bytes * (p.up ? 2u : 1u);
+        tx *= CG;
         s0 = s1 = x0 = x1 = nullptr;
-        half = 0;
+        sy = half = xy0 = xy1 = 0;
         if (SRC != kGroupBf16) {
             // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
             // (the second CTA of a pair may stand past the last row tile)
             const int64_t row_tile = n0 / kMxTileRows < p.w_row_tiles ? n0 / kMxTileRows : p.w_row_tiles - 1;
-            const int64_t at = ((int64_t)t.e * p.w_row_tiles + row_tile) * p.k_tiles * kMxTileBytes +
-                               (SRC == kGroupMxMx  ? (int64_t)kt * kMxTileBytes
-                                : SRC == kGroupMx8 ? (int64_t)kt * (kMxTileBytes / 2)
-                                                   : (int64_t)(kt >> 1) * (kMxTileBytes / 2));
+            const int64_t at = 2 * ((int64_t)t.e * p.w_row_tiles + row_tile) * p.k_tiles +
+                               (SRC == kGroupMxMx ? 2 * kt : SRC == kGroupMx8 ? kt : kt >> 1);
             half = kt & 1;
-            s0 = p.sw + at;
-            if (p.up) s1 = p.su + at;
+            s0 = p.sw + at * (kMxTileBytes / 2);
+            if (p.up) s1 = p.su + at * (kMxTileBytes / 2);
+            sy = (int)at;
         }
-        if (SRC == kGroupMx8) x0 = p.prep + (t.m * p.kt + kt) * p.prep_chunk;
+        if (SRC == kGroupMx8) {
+            const int64_t chunk = t.m * p.kt + kt;
+            x0 = p.prep + chunk * p.prep_chunk;
+            xy0 = (int)(chunk * (p.prep_chunk / 128));
+            xy1 = xy0 + (int)(p.sf_b_bytes / 128u) + rank * nN;
+        }
         if (SRC == kGroupMxMx) {
             // a row tile past the last reads the last one again (rows past the end: never stored)
             const int64_t rt = t.s0 / kMxTileRows, last = (p.x_rows - 1) / kMxTileRows;
-            x0 = p.sx + (rt * p.k_tiles + kt) * kMxTileBytes;
-            x1 = p.sx + ((rt < last ? rt + 1 : last) * p.k_tiles + kt) * kMxTileBytes;
+            const int64_t a0 = rt * p.k_tiles + kt, a1 = (rt < last ? rt + 1 : last) * p.k_tiles + kt;
+            x0 = p.sx + a0 * kMxTileBytes;
+            x1 = p.sx + a1 * kMxTileBytes;
+            xy0 = (int)(2 * a0);
+            xy1 = (int)(2 * a1);
         }
     }
-    __device__ __forceinline__ void weights(const GroupParams& p, const CUtensorMap& tm_w, uint32_t st, uint32_t fb) {
-        mbar_arrive_expect_tx(fb, tx);
-        tma_load_2d(st, &tm_w, ax, w0, fb);
-        tma_load_2d(st + kTileN / 2 * kARow, second, ax, w1, fb);
+    // scales of two weights, joined by kMix
+    __device__ static __forceinline__ bool joined(const GroupParams& p) { return SRC == kGroupMx8 && CG == 2 && p.up; }
+
+    // `lb`: the stage's barrier here, `fb`: the one that counts (pairs: the first CTA's), `sb`: that of the scales to be joined
+    __device__ __forceinline__ void weights(const GroupParams& p, const Maps& m, uint32_t st, uint32_t lb, uint32_t fb, uint32_t sb,
+                                            bool expect) {
+        if (expect) mbar_arrive_expect_tx(lb, tx);
+        if (joined(p)) {
+            mbar_arrive_expect_tx(sb, 2u * p.sf_a_bytes);
+            bulk_load(st + p.off_s, s0, p.sf_a_bytes, sb);
+            bulk_load(st + p.off_s + p.sf_a_bytes, s1, p.sf_a_bytes, sb);
+        }
+        load_box<CG>(st, &m.w, ax, w0, fb);
+        load_box<CG>(st + kTileN / 2 * kARow, second, ax, w1, fb);
         ax += SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2;
         if (SRC != kGroupBf16) {
-            bulk_load(st + p.off_s, s0, p.sf_a_bytes, fb);
-            if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, s1, p.sf_a_bytes, fb);
+            if (CG == 1) {
+                bulk_load(st + p.off_s, s0, p.sf_a_bytes, fb);
+                if (p.up) bulk_load(st + p.off_s + p.sf_a_bytes, s1, p.sf_a_bytes, fb);
+            } else if (!joined(p)) {
+                tma_load_pair(st + p.off_s, &m.sw, 0, sy, fb);
+            }
             const uint32_t step = SRC == kGroupMx && !half ? 0 : p.sf_a_bytes;
             s0 += step;
             s1 += step;
+            sy += SRC == kGroupMxMx ? 2 : 1;
             if (SRC == kGroupMx) half ^= 1;
         }
     }
-    __device__ __forceinline__ void rows(const GroupParams& p, const CUtensorMap& tm_x, uint32_t st, uint32_t fb,
-                                         const int4 (&idx)[8]) {
-        if (SRC == kGroupMx8) {   // scales and rows, one run in both memories
-            if (CG == 1) {
+    __device__ __forceinline__ void rows(const GroupParams& p, const Maps& m, uint32_t st, uint32_t fb, const int4 (&idx)[8]) {
+        if (SRC == kGroupMx8) {
+            if (CG == 1) {   // scales and rows, one run in both memories
                 bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes + x_bytes, fb);
-            } else {   // all columns' scales, this CTA's half of the rows
-                bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes, fb);
-                bulk_load(st + p.off_b, x0 + x_at, x_bytes, fb);
+                x0 += p.prep_chunk;
+            } else {         // all columns' scales, this CTA's half of the rows
+                tma_load_pair(st + p.off_b - p.sf_b_bytes, &m.sx, 0, xy0, fb);
+                for (int b = 0; b < boxes; b++) tma_load_pair(st + p.off_b + (uint32_t)(b * p.box) * 128u, &m.x, 0, xy1 + b * p.box, fb);
+                xy0 += (int)(p.prep_chunk / 128);
+                xy1 += (int)(p.prep_chunk / 128);
             }
-            x0 += p.prep_chunk;
             return;
         }
         if (SRC == kGroupMxMx) {
-            bulk_load(st + p.off_b - p.sf_b_bytes, x0, kMxTileBytes, fb);
-            if (p.sf_b_bytes > kMxTileBytes) bulk_load(st + p.off_b - kMxTileBytes, x1, kMxTileBytes, fb);
-            x0 += kMxTileBytes;
-            x1 += kMxTileBytes;
+            if (CG == 1) {
+                bulk_load(st + p.off_b - p.sf_b_bytes, x0, kMxTileBytes, fb);
+                if (p.sf_b_bytes > kMxTileBytes) bulk_load(st + p.off_b - kMxTileBytes, x1, kMxTileBytes, fb);
+                x0 += kMxTileBytes;
+                x1 += kMxTileBytes;
+            } else {
+                tma_load_pair(st + p.off_b - p.sf_b_bytes, &m.sx, 0, xy0, fb);
+                if (p.sf_b_bytes > kMxTileBytes) tma_load_pair(st + p.off_b - kMxTileBytes, &m.sx, 0, xy1, fb);
+                xy0 += 2;
+                xy1 += 2;
+            }
         }
         if (gathers) {
 #pragma unroll
             for (int g = 0; g < 8; g++)
-                if (g < gathers) tma_gather4(st + p.off_b + (uint32_t)g * 512u, &tm_x, bx, idx[g], fb);
+                if (g < gathers) tma_gather4(st + p.off_b + (uint32_t)g * 512u, &m.x, bx, idx[g], fb);
         } else {
-            for (int b = 0; b < boxes; b++) tma_load_2d(st + p.off_b + (uint32_t)(b * p.box) * 128u, &tm_x, bx, y + b * p.box, fb);
+            for (int b = 0; b < boxes; b++) load_box<CG>(st + p.off_b + (uint32_t)(b * p.box) * 128u, &m.x, bx, y + b * p.box, fb);
         }
         bx += SRC == kGroupMxMx ? KB / 2 : KB;
     }
 };
 
 template <int SRC, int CG>
-__device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_u,
-                                           const GroupParams& p) {
+__device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) {
     constexpr int KB = stage_k(SRC);
     constexpr bool kRe = SRC == kGroupMx;
     constexpr bool kScaled = SRC == kGroupMx8 || SRC == kGroupMxMx;   // scales in tensor memory
@@ -634,7 +689,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ctrl_off);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxS, recon = empty + 8 * kMaxS, tfree = recon + 8 * kMaxT;
-    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8, peer = mixed + 8 * kMaxS;
+    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8, joins = mixed + 8 * kMaxS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * kMaxS + 2 * kMaxT + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* cum = reinterpret_cast<int32_t*>(smem + p.tab_off);
@@ -647,10 +702,10 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.S; s++) {
-            mbar_init(peer + 8 * s, 1);
+            mbar_init(joins + 8 * s, 1);
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
-            mbar_init(mixed + 8 * s, 1);
+            mbar_init(mixed + 8 * s, CG);
         }
         for (int t = 0; t < p.T; t++) {
             mbar_init(recon + 8 * t, kRebuildWarps);
@@ -666,9 +721,9 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     }
     if (warp == kMma) pair_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
     if (warp == kProd && lane == 0) {
-        tma_prefetch_desc(&tm_x);
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_u);
+        tma_prefetch_desc(&m.w);
+        if (p.up) tma_prefetch_desc(&m.u);
+        if (SRC != kGroupMx8 || CG == 2) tma_prefetch_desc(&m.x);
     }
     // With a preparing kernel before this one the offsets and weights are
     // complete already (see k_group_split); what it writes is waited for below.
@@ -713,14 +768,17 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
         // One thread walks the stages.
         if (elect_one()) {
         int64_t q = 0, pre = 0;
+        const uint32_t sig = CG == 2 ? in_first(full) - full : 0;   // from a barrier here to the first CTA's
+        const bool expect = rank == 0;
         Seg sg;
         if (p.early) {
             // the first stages' weights and scales, before the wait on the preparing kernel
             Walk w0(pl, worker);
             while (pre < p.S && w0.next(pl, p.kt, sg)) {
-                Feed<SRC, CG> f(p, tm_w, tm_u, locate(p, pl, sg.tile), sg.kt0, rank);
+                Feed<SRC, CG> f(p, m, locate(p, pl, sg.tile), sg.kt0, rank);
                 for (int kt = sg.kt0; kt < sg.kt1 && pre < p.S; kt++, pre++)
-                    f.weights(p, tm_w, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre);
+                    f.weights(p, m, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre, full + 8 * (uint32_t)pre + sig,
+                              joins + 8 * (uint32_t)pre, expect);
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
         }
@@ -744,15 +802,15 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
                 if (wrong) raise_status(UW_ERR_DEVICE);
             }
-            Feed<SRC, CG> f(p, tm_w, tm_u, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0,
+            Feed<SRC, CG> f(p, m, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0,
                             rank);
-            Feed<SRC, CG> x(p, tm_w, tm_u, t, sg.kt0, rank);
+            Feed<SRC, CG> x(p, m, t, sg.kt0, rank);
             for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                 if (q >= pre) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
-                    f.weights(p, tm_w, st, fb);
+                    f.weights(p, m, st, fb, fb + sig, fb + (joins - full), expect);
                 }
-                x.rows(p, tm_x, st, fb, idx);
+                x.rows(p, m, st, fb + sig, idx);
                 st += p.stage_bytes;
                 fb += 8;
                 if (++slot == p.S) {
@@ -763,7 +821,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                 }
             }
         }
-        if (!ok)   // every load already issued lands before the CTA exits
+        if (!ok && rank == 0)   // every load already issued lands before the CTA (or the pair) exits
             for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
                 mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
         }
@@ -771,29 +829,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
     } else if (warp == kMma) {
         // ------------------------------------------------------------ MMA issue
         // One thread walks the stages; descriptors and barriers advance with the slot.
-        if (CG == 2 && rank == 1) {
-            // the pair's second CTA tells the first which of its stages have landed
-            if (elect_one()) {
-                Walk wk(pl, worker);
-                Seg sg;
-                int slot = 0;
-                uint32_t ph = 0, fb = full;
-                const uint32_t to = in_first(peer) - full;
-                bool ok = true;
-                while (ok && wk.next(pl, p.kt, sg))
-                    for (int kt = sg.kt0; kt < sg.kt1; kt++) {
-                        if (SRC == kGroupMx8 && p.up && !wait_one(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
-                        if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
-                        arrive_at(fb + to);
-                        fb += 8;
-                        if (++slot == p.S) {
-                            slot = 0;
-                            ph ^= 1u;
-                            fb = full;
-                        }
-                    }
-            }
-        } else if (elect_one()) {
+        // In a pair the first CTA's thread issues for both.
+        if (rank == 0 && elect_one()) {
         constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // sw128_desc's upper word
         const uint32_t lo0 = ((base >> 4) & 0x3FFFu) | (1u << 16), lo_step = p.stage_bytes >> 4, lo_b = p.off_b >> 4;
         auto desc = [](uint32_t lo) { return ((uint64_t)kHi << 32) | lo; };
@@ -815,9 +852,8 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             uint32_t more = 0;   // 0: the tile's first MMA overwrites
             for (int kt = sg.kt0; kt < sg.kt1; kt++) {
                 if (kRe && !wait_one(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (SRC == kGroupMx8 && p.up && !wait_one(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
+                if (SRC == kGroupMx8 && p.up && !wait_pair<CG>(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (CG == 2 && !wait_pair<CG>(fb + (peer - full), ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (kScaled) {
                     // scales of the stage, 4 columns per 512 bytes: weights, then rows
@@ -894,7 +930,7 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
             while (ok && wk.next(pl, p.kt, sg)) {
                 const Tile t = locate(p, pl, sg.tile);
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
-                    if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
                     const uint32_t at = ss + (uint32_t)(lane * 16 + ((t.n * CG + rank) & 1) * 8);
                     const uint32_t to = ss + 1024u + (uint32_t)(lane * 16);
@@ -905,7 +941,10 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(mixed + 8 * r.i);
+                    if (lane == 0) {
+                        if (CG == 2) arrive_at(in_first(mixed + 8 * r.i));
+                        else mbar_arrive(mixed + 8 * r.i);
+                    }
                 }
             }
         }
@@ -1089,15 +1128,13 @@ __device__ __forceinline__ void group_body(const CUtensorMap& tm_x, const CUtens
 
 template <int SRC, int CG>
 __global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
-    k_group(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-            const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<SRC, CG>(tm_x, tm_w, tm_u, p);
+    k_group(const __grid_constant__ Maps m, const GroupParams p) {
+    group_body<SRC, CG>(m, p);
 }
 
 __global__ void __launch_bounds__(kThreadsRebuild, 1)
-    k_group_rebuild(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_u, const GroupParams p) {
-    group_body<kGroupMx, 1>(tm_x, tm_w, tm_u, p);
+    k_group_rebuild(const __grid_constant__ Maps m, const GroupParams p) {
+    group_body<kGroupMx, 1>(m, p);
 }
 
 // ---------------------------------------------------------------- rows before the product
@@ -1370,7 +1407,9 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.kt = h.kt;
     p.MG = MG;
     const int CG = h.CG;
-    p.box = MG / CG % 64 ? MG / CG : 64;   // divides MG / CG: boxes never pass the rows set aside
+    // divides MG / CG: boxes never pass the rows set aside.  (Split rows: one box whatever the tile holds; seven of
+    // 16 rows cost the producer more than the bytes: 4480 x 8192 x 4096 248 us against XXX.)
+    p.box = src == kGroupMx8 ? MG : MG / CG % 64 ? MG / CG : 64;
     p.up = a.up ? 1 : 0;
     p.n_tiles = h.n_tiles;
     p.out_f32 = a.out_f32;
@@ -1424,32 +1463,42 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.tab_off = p.stg_off + epi;
     const size_t smem = (size_t)S * p.stage_bytes + fixed;
 
-    CUtensorMap tx{}, tw{}, tu{};
+    Maps m{};
     bool ok = true;
     const uint64_t wrows = (uint64_t)a.E * (uint64_t)a.N;
     if (src == kGroupMxMx)
-        ok = make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, a.K / 2, a.x_rows, a.K / 2, 128, p.box,
+        ok = make_map_2d(&m.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, a.K / 2, a.x_rows, a.K / 2, 128, p.box,
                          CU_TENSOR_MAP_SWIZZLE_128B);
     else if (src != kGroupMx8)
-        ok = make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.gather ? (const void*)prep : a.X, a.K,
+        ok = make_map_2d(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.gather ? (const void*)prep : a.X, a.K,
                          h.gather ? a.slots : a.x_rows, a.K * 2, 64, p.rows ? 1 : p.box, CU_TENSOR_MAP_SWIZZLE_128B);
-    for (int i = 0; i < 2; i++) {
-        const void* w = i && a.up ? a.up : a.W;
-        CUtensorMap* m = i ? &tu : &tw;
+    else if (CG == 2)   // prepared rows: 128 bytes each, swizzled already
+        ok = make_map_2d(&m.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, prep, 128, h.prep / 128, 128, 128, p.box, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+             make_map_2d(&m.sx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, prep, 128, h.prep / 128, 128, 128, h.sf_b / 128,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
+    const uint32_t halves = src == kGroupMxMx ? 2 : 1;   // half scale tiles of a stage
+    if (src == kGroupMxMx && CG == 2)
+        ok = ok && make_map_2d(&m.sx, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.x_scales, 128,
+                               2 * (uint64_t)mx_row_tiles(a.x_rows) * p.k_tiles, 512, 128, halves, CU_TENSOR_MAP_SWIZZLE_NONE);
+    for (int i = 0; i < (a.up ? 2 : 1); i++) {
+        const void* w = i ? a.up : a.W;
+        CUtensorMap* mw = i ? &m.u : &m.w;
         if (src == kGroupBf16)
-            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, a.K, wrows, a.K * 2, 64, kTileN / 2,
+            ok = ok && make_map_2d(mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, a.K, wrows, a.K * 2, 64, kTileN / 2,
                                    CU_TENSOR_MAP_SWIZZLE_128B);
         else if (src == kGroupMx8)   // 16 packed codes -> 16 bytes of shared memory
-            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 1, w, a.K, wrows, a.K / 2, 128, kTileN / 2,
+            ok = ok && make_map_2d(mw, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 1, w, a.K, wrows, a.K / 2, 128, kTileN / 2,
                                    CU_TENSOR_MAP_SWIZZLE_128B);
         else
-            ok = ok && make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.K / 2, wrows, a.K / 2, src == kGroupMx ? 32 : 128,
+            ok = ok && make_map_2d(mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.K / 2, wrows, a.K / 2, src == kGroupMx ? 32 : 128,
                                    kTileN / 2, src == kGroupMx ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B);
     }
+    if (CG == 2 && src != kGroupBf16 && !a.up)
+        ok = ok && make_map_2d(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.w_scales, 128, 2 * (uint64_t)a.E * p.w_row_tiles * p.k_tiles,
+                               512, 128, halves, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) { *st = UW_ERR_CUDA; return cudaSuccess; }
-    if (src == kGroupMx8) tx = tw;   // unused
 
-    void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupParams) =
+    void (*kern)(const Maps, const GroupParams) =
         src == kGroupBf16   ? (CG == 2 ? k_group<kGroupBf16, 2> : k_group<kGroupBf16, 1>)
         : src == kGroupMxMx ? (CG == 2 ? k_group<kGroupMxMx, 2> : k_group<kGroupMxMx, 1>)
         : src == kGroupMx8  ? (CG == 2 ? k_group<kGroupMx8, 2> : k_group<kGroupMx8, 1>)
@@ -1481,7 +1530,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     }
     const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
     return launch_after(kern, dim3((unsigned)(workers * CG)), CG,
-                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 ? kThreadsMix : kThreadsPlain, smem, s, tx, tw, tu, p);
+                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 ? kThreadsMix : kThreadsPlain, smem, s, m, p);
 }
 
 }  // namespace uw
