@@ -20,8 +20,8 @@
 //     a worker; what is left over is cut along k (see Plan).  The worker with a
 //     cut tile's first k steps adds the others' fp32 partial sums in k order
 //     (from the workspace; deterministic);
-//   * warp roles: 0-7 epilogue, 8 TMA producer, 9 MMA issue (10: see kMix;
-//     12-19: see kGroupMx);
+//   * warp roles: 0-7 epilogue, 8 and 11 TMA producers of weights and of X, 9 MMA
+//     issue (10: see kMix; 12-19: see kGroupMx);
 //   * 4-bit weights with BF16 rows (kGroupMx8): the tensor cores take the codes
 //     and scales as they are, against 8-bit rows.  A BF16 value has 8
 //     significant bits, an e4m3 value 4: x = 2^s (hi + lo/16) with both in
@@ -62,8 +62,8 @@ constexpr int kTileN = 128;            // weight rows of a tile
 constexpr int kProd = 8, kMma = 9, kRebuild0 = 12, kRebuildWarps = 8;
 constexpr int kEpiWarps = 8;           // two per quarter of tensor memory's lanes
 constexpr int kMix = 10;               // kGroupMx8: warp that joins the scales of two weights
-constexpr int kThreadsPlain = 10 * 32;
-constexpr int kThreadsMix = 11 * 32;
+constexpr int kRows = 11;              // TMA producer of X
+constexpr int kThreadsPlain = 12 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
 constexpr int kMaxS = 12;              // stages
 constexpr int kMaxT = 8;               // rebuilt-A slots in tensor memory
@@ -734,6 +734,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     if (CG == 2) cluster_sync();   // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (the weights' producer goes ahead: everything it reads is complete)
     if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     Plan pl;
@@ -764,66 +765,77 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     const int rows_a = p.up ? kTileN / 2 : kTileN;   // outputs of a tile
 
     if (warp == kProd) {
-        // ------------------------------------------------------------ TMA producer
-        // One thread walks the stages.
+        // ------------------------------------------------------------ TMA producer: weights and their scales
+        // One thread walks the stages.  X has a thread of its own (below): one
+        // thread for both took 500 cycles a stage of 4-bit weights, more than
+        // its MMAs, and 1700 where the tile changes.
         if (elect_one()) {
-        int64_t q = 0, pre = 0;
-        const uint32_t sig = CG == 2 ? in_first(full) - full : 0;   // from a barrier here to the first CTA's
-        const bool expect = rank == 0;
-        Seg sg;
-        if (p.early) {
-            // the first stages' weights and scales, before the wait on the preparing kernel
-            Walk w0(pl, worker);
-            while (pre < p.S && w0.next(pl, p.kt, sg)) {
+            Walk wk(pl, worker);
+            Seg sg;
+            int slot = 0;
+            int64_t q = 0;
+            uint32_t ph = 1, st = base, fb = full;
+            const uint32_t sig = CG == 2 ? in_first(full) - full : 0;   // from a barrier here to the first CTA's
+            bool ok = true;
+            while (ok && wk.next(pl, p.kt, sg)) {
                 Feed<SRC, CG> f(p, m, locate(p, pl, sg.tile), sg.kt0, rank);
-                for (int kt = sg.kt0; kt < sg.kt1 && pre < p.S; kt++, pre++)
-                    f.weights(p, m, base + (uint32_t)pre * p.stage_bytes, full + 8 * (uint32_t)pre, full + 8 * (uint32_t)pre + sig,
-                              joins + 8 * (uint32_t)pre, expect);
-            }
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-        }
-        Walk wk(pl, worker);
-        int slot = 0;
-        uint32_t ph = 1, st = base, fb = full;
-        bool ok = true;
-        while (ok && wk.next(pl, p.kt, sg)) {
-            const Tile t = locate(p, pl, sg.tile);
-            int4 idx[8];
-            if (p.rows) {
-                // four rows a request; past the tile's end its last row again (never stored)
-                int* ip = &idx[0].x;
-                bool wrong = false;
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    const int32_t v = p.rows[t.s0 + (i < t.rows ? i : t.rows - 1)];
-                    const bool in = v >= 0 && v < p.x_rows;
-                    wrong |= !in;
-                    ip[i] = in ? v : 0;
-                }
-                if (wrong) raise_status(UW_ERR_DEVICE);
-            }
-            Feed<SRC, CG> f(p, m, t, q < pre ? (int)(sg.kt0 + (pre - q < sg.kt1 - sg.kt0 ? pre - q : sg.kt1 - sg.kt0)) : sg.kt0,
-                            rank);
-            Feed<SRC, CG> x(p, m, t, sg.kt0, rank);
-            for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
-                if (q >= pre) {
+                for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
-                    f.weights(p, m, st, fb, fb + sig, fb + (joins - full), expect);
-                }
-                x.rows(p, m, st, fb + sig, idx);
-                st += p.stage_bytes;
-                fb += 8;
-                if (++slot == p.S) {
-                    slot = 0;
-                    ph ^= 1u;
-                    st = base;
-                    fb = full;
+                    f.weights(p, m, st, fb, fb + sig, fb + (joins - full), rank == 0);
+                    st += p.stage_bytes;
+                    fb += 8;
+                    if (++slot == p.S) {
+                        slot = 0;
+                        ph ^= 1u;
+                        st = base;
+                        fb = full;
+                    }
                 }
             }
+            if (!ok && rank == 0)   // every load already issued lands before the CTA (or the pair) exits
+                for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
+                    mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
         }
-        if (!ok && rank == 0)   // every load already issued lands before the CTA (or the pair) exits
-            for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
-                mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
+        __syncwarp();
+    } else if (warp == kRows) {
+        // ------------------------------------------------------------ TMA producer: X
+        if (elect_one()) {
+            Walk wk(pl, worker);
+            Seg sg;
+            int slot = 0;
+            uint32_t ph = 1, st = base, fb = full;
+            const uint32_t sig = CG == 2 ? in_first(full) - full : 0;
+            bool ok = true;
+            while (ok && wk.next(pl, p.kt, sg)) {
+                const Tile t = locate(p, pl, sg.tile);
+                Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
+                int4 idx[8];
+                if (CG == 1 && p.rows) {
+                    // four rows a request; past the tile's end its last row again (never stored)
+                    int* ip = &idx[0].x;
+                    bool wrong = false;
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const int32_t v = p.rows[t.s0 + (i < t.rows ? i : t.rows - 1)];
+                        const bool in = v >= 0 && v < p.x_rows;
+                        wrong |= !in;
+                        ip[i] = in ? v : 0;
+                    }
+                    if (wrong) raise_status(UW_ERR_DEVICE);
+                }
+                for (int kt = sg.kt0; kt < sg.kt1; kt++) {
+                    if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
+                    f.rows(p, m, st, fb + sig, idx);
+                    st += p.stage_bytes;
+                    fb += 8;
+                    if (++slot == p.S) {
+                        slot = 0;
+                        ph ^= 1u;
+                        st = base;
+                        fb = full;
+                    }
+                }
+            }
         }
         __syncwarp();
     } else if (warp == kMma) {
@@ -1127,7 +1139,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 }
 
 template <int SRC, int CG>
-__global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
+__global__ void __launch_bounds__(kThreadsPlain, 1)
     k_group(const __grid_constant__ Maps m, const GroupParams p) {
     group_body<SRC, CG>(m, p);
 }
@@ -1530,7 +1542,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     }
     const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
     return launch_after(kern, dim3((unsigned)(workers * CG)), CG,
-                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 ? kThreadsMix : kThreadsPlain, smem, s, m, p);
+                        src == kGroupMx ? kThreadsRebuild : kThreadsPlain, smem, s, m, p);
 }
 
 }  // namespace uw
