@@ -69,7 +69,7 @@ constexpr int kMaxS = 12;              // stages
 constexpr int kMaxT = 8;               // rebuilt-A slots in tensor memory
 constexpr int kBand = 16;              // slot tiles of a band
 constexpr int kEpiBarId = 1;
-constexpr uint32_t kWarpStage = 1024;  // transpose buffer of an epilogue warp
+constexpr uint32_t kWarpStage = 2048;  // transpose buffer of an epilogue warp
 constexpr uint32_t kExchange = kEpiWarps * 2048;   // `up`: 16 slots x 32 rows of fp32 sums a warp
 constexpr uint32_t kTmemCols = 512;
 
@@ -98,7 +98,7 @@ struct GroupParams {
     const uint8_t* prep;                    // kGroupMx8: [slot tiles][kt][scales, rows]
     int64_t prep_chunk;                     // bytes of one stage of one tile there
     int part_f4;                            // float4 columns of a partial row
-    uint32_t ctrl_off, stg_off, tab_off;
+    uint32_t ctrl_off, stg_off, tab_off, work_off;
     const uint8_t* sw;                      // scale tiles of W, up, X
     const uint8_t* su;
     const uint8_t* sx;
@@ -164,46 +164,44 @@ struct Tile {
 __device__ __forceinline__ int64_t unit_begin(int64_t b, const Plan& pl) { return b * pl.units / pl.ps; }
 __device__ __forceinline__ int unit_owner(int64_t u, const Plan& pl) { return (int)(((u + 1) * pl.ps - 1) / pl.units); }
 
-// A worker's segments: its range or part of the cut tiles first (joining them
+// Segment i of worker b: its range or part of the cut tiles first (joining them
 // then overlaps the whole tiles), then its whole tiles.
-struct Walk {
-    int64_t u, ue, t;
-    int part, own;
-    __device__ __forceinline__ Walk(const Plan& pl, int b) {
-        u = ue = 0;
-        if (b < pl.ps) {
-            u = unit_begin(b, pl);
-            ue = unit_begin(b + 1, pl);
-        }
-        t = b;
-        part = pl.parts && b < pl.parts * pl.rest ? b / pl.rest : -1;
-        own = part > 0 ? b - part * pl.rest : b;
-    }
-    __device__ __forceinline__ bool next(const Plan& pl, int kt, Seg& s) {
-        if (u < ue) {
-            s.tile = pl.whole + u / kt;
-            s.kt0 = (int)(u % kt);
-            const int64_t left = ue - u;
-            s.kt1 = left < kt - s.kt0 ? s.kt0 + (int)left : kt;
-            u += s.kt1 - s.kt0;
+__device__ __forceinline__ bool segment(const Plan& pl, int b, int i, int kt, Seg& s) {
+    if (b < pl.ps) {
+        const int64_t u0 = unit_begin(b, pl), ue = unit_begin(b + 1, pl);
+        const int64_t t0 = u0 / kt;
+        const int n = ue > u0 ? (int)((ue - 1) / kt - t0) + 1 : 0;
+        if (i < n) {
+            const int64_t first = i ? (t0 + i) * kt : u0, end = (t0 + i + 1) * kt < ue ? (t0 + i + 1) * kt : ue;
+            s.tile = pl.whole + t0 + i;
+            s.kt0 = (int)(first - (t0 + i) * kt);
+            s.kt1 = (int)(end - (t0 + i) * kt);
             return true;
         }
-        if (part >= 0) {
-            s.tile = pl.whole + own;
+        i -= n;
+    } else if (b < pl.parts * pl.rest) {
+        if (i == 0) {
+            const int part = b / pl.rest;
+            s.tile = pl.whole + b % pl.rest;
             s.kt0 = part * kt / pl.parts;
             s.kt1 = (part + 1) * kt / pl.parts;
-            part = -1;
             return true;
         }
-        if (t < pl.whole) {
-            s.tile = t;
-            s.kt0 = 0;
-            s.kt1 = kt;
-            t += pl.P;
-            return true;
-        }
-        return false;
+        i--;
     }
+    s.tile = b + (int64_t)i * pl.P;
+    s.kt0 = 0;
+    s.kt1 = kt;
+    return s.tile < pl.whole;
+}
+
+// A worker's segments with their tiles.  The first kListed are worked out by
+// the block's threads at once when it starts (in every role, one after the
+// other, they cost 1700 cycles a tile).
+constexpr int kListed = 40;
+struct Work {
+    Seg seg;
+    Tile tile;
 };
 
 __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int64_t tile) {
@@ -229,6 +227,24 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int
     return t;
 }
 
+struct Walk {
+    const Work* list;
+    int worker, i = 0;
+    __device__ __forceinline__ Walk(const Work* l, int b) : list(l), worker(b) {}
+    __device__ __forceinline__ bool next(const GroupParams& p, const Plan& pl, Seg& s, Tile& t) {
+        if (i < kListed) {
+            s = list[i].seg;
+            t = list[i].tile;
+            i++;
+            return t.rows > 0;
+        }
+        if (!segment(pl, worker, i, p.kt, s)) return false;
+        i++;
+        t = locate(p, pl, s.tile);
+        return true;
+    }
+};
+
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -240,24 +256,22 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
 // BF16 through 1 KB of shared memory and leave as 16-byte stores, four lanes a
 // slot.  Rows of N values that are not 16-byte aligned (N % 8) are stored value
 // by value, and so is fp32 (128 contiguous bytes a slot already).
-__device__ __forceinline__ void store16(const GroupParams& p, const uint32_t (&v)[16], int64_t s0, int valid, int64_t nw, int lane,
-                                        uint32_t stg) {
-    if (p.out_f32 || !p.y_vec) {
-        if (nw + lane >= p.N) return;
-        const int64_t at = s0 * p.N + nw + lane;
+__device__ __forceinline__ void put_plain(const GroupParams& p, const uint32_t (&v)[16], int64_t s0, int valid, int64_t nw, int lane) {
+    if (nw + lane >= p.N) return;
+    const int64_t at = s0 * p.N + nw + lane;
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            if (i < valid) {
-                if (p.out_f32) reinterpret_cast<float*>(p.Y)[at + i * p.N] = __uint_as_float(v[i]);
-                else reinterpret_cast<__nv_bfloat16*>(p.Y)[at + i * p.N] = __float2bfloat16_rn(__uint_as_float(v[i]));
-            }
-        return;
-    }
-    __syncwarp();   // the buffer's last readers are through
+    for (int i = 0; i < 16; i++)
+        if (i < valid) {
+            if (p.out_f32) reinterpret_cast<float*>(p.Y)[at + i * p.N] = __uint_as_float(v[i]);
+            else reinterpret_cast<__nv_bfloat16*>(p.Y)[at + i * p.N] = __float2bfloat16_rn(__uint_as_float(v[i]));
+        }
+}
+__device__ __forceinline__ void stage16(const uint32_t (&v)[16], int lane, uint32_t stg) {
 #pragma unroll
     for (int i = 0; i < 8; i++) sts32(stg + (uint32_t)(i * 128 + lane * 4), bf2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
-    __syncwarp();
-    // lane: slots 2 (lane / 4) and the next, outputs 8 (lane % 4) ..
+}
+// (lane: slots 2 (lane / 4) and the next, outputs 8 (lane % 4) ..)
+__device__ __forceinline__ void put16(const GroupParams& p, int64_t s0, int valid, int64_t nw, int lane, uint32_t stg) {
     const int s = (lane >> 2) * 2, o = (lane & 3) * 8;
     const uint4 a = lds128(stg + (uint32_t)((lane >> 2) * 128 + (lane & 3) * 32));
     const uint4 b = lds128(stg + (uint32_t)((lane >> 2) * 128 + (lane & 3) * 32 + 16));
@@ -268,6 +282,32 @@ __device__ __forceinline__ void store16(const GroupParams& p, const uint32_t (&v
     if (s + 1 < valid)
         *reinterpret_cast<uint4*>(y + p.N) =
             make_uint4(prmt(a.x, a.y, 0x7632u), prmt(a.z, a.w, 0x7632u), prmt(b.x, b.y, 0x7632u), prmt(b.z, b.w, 0x7632u));
+}
+__device__ __forceinline__ void store16(const GroupParams& p, const uint32_t (&v)[16], int64_t s0, int valid, int64_t nw, int lane,
+                                        uint32_t stg) {
+    if (p.out_f32 || !p.y_vec) {
+        put_plain(p, v, s0, valid, nw, lane);
+        return;
+    }
+    __syncwarp();   // the buffer's last readers are through
+    stage16(v, lane, stg);
+    __syncwarp();
+    put16(p, s0, valid, nw, lane, stg);
+}
+// 32 slots (16 unless `two`) in one go.
+__device__ __forceinline__ void store32(const GroupParams& p, const uint32_t (&v)[2][16], bool two, int64_t s0, int valid, int64_t nw,
+                                        int lane, uint32_t stg) {
+    if (p.out_f32 || !p.y_vec) {
+        put_plain(p, v[0], s0, valid, nw, lane);
+        if (two) put_plain(p, v[1], s0 + 16, valid - 16, nw, lane);
+        return;
+    }
+    __syncwarp();
+    stage16(v[0], lane, stg);
+    if (two) stage16(v[1], lane, stg + 1024u);
+    __syncwarp();
+    put16(p, s0, valid, nw, lane, stg);
+    if (two) put16(p, s0 + 16, valid - 16, nw, lane, stg + 1024u);
 }
 
 __device__ __forceinline__ bool any_of_epilogue(bool pred) {
@@ -490,9 +530,6 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-__device__ __forceinline__ void release_at(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
 __device__ __forceinline__ bool test_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -528,7 +565,15 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t t
     return mbar_wait(bar, parity, timeout, abort);
 }
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint64_t timeout, volatile int* abort) {
-    return mbar_try_wait(bar, parity, 1000) || wait_slow(bar, parity, timeout, abort);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0 || mbar_try_wait(bar, parity, 1000) || wait_slow(bar, parity, timeout, abort);
 }
 // The same for a barrier on which the pair's other CTA arrives too.
 template <int CG>
@@ -734,8 +779,6 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     if (CG == 2) cluster_sync();   // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (the weights' producer goes ahead: everything it reads is complete)
-    if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     Plan pl;
     pl.cum = cum;
@@ -762,6 +805,16 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             pl.ps = (int)(P < most ? P : most);
         }
     }
+    Work* work = reinterpret_cast<Work*>(smem + p.work_off);
+    for (int i = threadIdx.x; i < kListed; i += blockDim.x) {
+        Work w;
+        if (segment(pl, worker, i, p.kt, w.seg)) w.tile = locate(p, pl, w.seg.tile);
+        else w.tile.rows = 0;
+        work[i] = w;
+    }
+    __syncthreads();
+    // (the weights' producer goes ahead: everything it reads is complete)
+    if (p.early && warp != kProd) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int rows_a = p.up ? kTileN / 2 : kTileN;   // outputs of a tile
 
     if (warp == kProd) {
@@ -770,15 +823,16 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         // thread for both took 500 cycles a stage of 4-bit weights, more than
         // its MMAs, and 1700 where the tile changes.
         if (elect_one()) {
-            Walk wk(pl, worker);
+            Walk wk(work, worker);
             Seg sg;
             int slot = 0;
             int64_t q = 0;
             uint32_t ph = 1, st = base, fb = full;
             const uint32_t sig = CG == 2 ? in_first(full) - full : 0;   // from a barrier here to the first CTA's
             bool ok = true;
-            while (ok && wk.next(pl, p.kt, sg)) {
-                Feed<SRC, CG> f(p, m, locate(p, pl, sg.tile), sg.kt0, rank);
+            Tile t;
+            while (ok && wk.next(p, pl, sg, t)) {
+                Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
                     f.weights(p, m, st, fb, fb + sig, fb + (joins - full), rank == 0);
@@ -800,14 +854,14 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     } else if (warp == kRows) {
         // ------------------------------------------------------------ TMA producer: X
         if (elect_one()) {
-            Walk wk(pl, worker);
+            Walk wk(work, worker);
             Seg sg;
             int slot = 0;
             uint32_t ph = 1, st = base, fb = full;
             const uint32_t sig = CG == 2 ? in_first(full) - full : 0;
             bool ok = true;
-            while (ok && wk.next(pl, p.kt, sg)) {
-                const Tile t = locate(p, pl, sg.tile);
+            Tile t;
+            while (ok && wk.next(p, pl, sg, t)) {
                 Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
                 int4 idx[8];
                 if (CG == 1 && p.rows) {
@@ -846,14 +900,14 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // sw128_desc's upper word
         const uint32_t lo0 = ((base >> 4) & 0x3FFFu) | (1u << 16), lo_step = p.stage_bytes >> 4, lo_b = p.off_b >> 4;
         auto desc = [](uint32_t lo) { return ((uint64_t)kHi << 32) | lo; };
-        Walk wk(pl, worker);
+        Walk wk(work, worker);
         Seg sg;
         Ring rt, ra;
         int slot = 0;
         uint32_t ph = 0, fb = full, lo = lo0, sf = tmem + p.sf_col0;
         bool ok = true;
-        while (ok && wk.next(pl, p.kt, sg)) {
-            const Tile t = locate(p, pl, sg.tile);
+        Tile t;
+        while (ok && wk.next(p, pl, sg, t)) {
             const int nN = mma_n<SRC, CG>(t.rows);
             const uint32_t idesc = SRC == kGroupMx8    ? idesc_mx8(CG, nN, 0)
                                    : SRC == kGroupMxMx ? idesc_mx(CG, nN, 0)
@@ -935,12 +989,12 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
         // either into the 16 bytes that tensor memory takes for lane l.
         if (p.up) {
-            Walk wk(pl, worker);
+            Walk wk(work, worker);
             Seg sg;
             Ring r;
             bool ok = true;
-            while (ok && wk.next(pl, p.kt, sg)) {
-                const Tile t = locate(p, pl, sg.tile);
+            Tile t;
+            while (ok && wk.next(p, pl, sg, t)) {
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
                     if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
@@ -966,12 +1020,12 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         // warps of a quarter take one piece of 32 k each.
         const int quarter = warp & 3, pc = (warp - kRebuild0) >> 2;
         const int row = 32 * quarter + lane;
-        Walk wk(pl, worker);
+        Walk wk(work, worker);
         Seg sg;
         Ring r, rt;
         bool ok = true;
-        while (ok && wk.next(pl, p.kt, sg)) {
-            const Tile t = locate(p, pl, sg.tile);
+        Tile t;
+        while (ok && wk.next(p, pl, sg, t)) {
             // where this row's scale bytes are in the stage
             uint32_t so = p.off_s;
             int sq = quarter;
@@ -999,18 +1053,18 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         }
     } else if (warp < kEpiWarps) {
         // ------------------------------------------------------------ epilogue
-        // Warps q and q + 4 share the tile's rows 32 q ..; of every 32 slots the
-        // first takes 16 and the second 16 (with `up`: of every 64, 32 each).
+        // Warps q and q + 4 share the tile's rows 32 q ..; of every 64 slots each
+        // takes 32.
         const int quarter = warp & 3, set = warp >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t stg = base + p.stg_off + (uint32_t)warp * kWarpStage, xch = base + p.stg_off + kEpiWarps * kWarpStage;
         const size_t slot_f4 = (size_t)p.part_f4 * kTileN;   // float4s of a CTA's partial
-        Walk wk(pl, worker);
+        Walk wk(work, worker);
         Seg sg;
         Ring ra;
-        while (wk.next(pl, p.kt, sg)) {
-            const Tile t = locate(p, pl, sg.tile);
+        Tile t;
+        while (wk.next(p, pl, sg, t)) {
             const int cols = (t.rows + 15) & ~15;
             const uint32_t lo = (uint32_t)(mma_n<SRC, CG>(t.rows) / 2);   // split rows: first lo column
             const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
@@ -1025,6 +1079,17 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             if (any_of_epilogue(!good)) break;
             tc_fence_after();
             const uint32_t acc = trow + (uint32_t)ra.i * p.acc_w;
+            // The accumulator is free once this warp has read its share.  (An arrival in the pair's first CTA orders nothing by
+            // itself: the loads are complete, which is all that the MMAs that overwrite it need.  At cluster scope a release
+            // would cost about 1600 cycles a tile.)
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) arrive_at(in_first(acce + 8 * ra.i));
+                    else mbar_arrive(acce + 8 * ra.i);
+                }
+            };
             // 16 slots of the accumulator (hi + lo of split rows)
             auto take = [&](int c, uint32_t (&v)[16]) {
                 tmem_ld16(acc + (uint32_t)c, v);
@@ -1041,7 +1106,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             if (publish) {
                 float4* dst = reinterpret_cast<float4*>(p.partial) + (size_t)blockIdx.x * slot_f4 + row;
                 for (int c = 0; c < cols; c += 16) {
-                    if ((c >> (p.up ? 5 : 4) & 1) != set) continue;
+                    if ((c >> 5 & 1) != set) continue;
                     uint32_t v[16];
                     take(c, v);
 #pragma unroll
@@ -1050,6 +1115,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
                 }
+                release();
                 __threadfence();
                 __syncwarp();
                 if (lane == 0)
@@ -1058,28 +1124,48 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                                  : "memory");
             } else {
                 // 16 slots of the finished sum: the accumulator plus the other ranges' partial sums, in k order
+                // (two ranges' loads at a time)
                 auto sum = [&](int c, uint32_t (&v)[16]) {
                     take(c, v);
-                    for (int b = worker + stride; b <= last; b += stride) {
-                        const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row;
+                    for (int b = worker + stride; b <= last; b += 2 * stride) {
+                        const float4* src = reinterpret_cast<const float4*>(p.partial) + (size_t)(b * CG + rank) * slot_f4 + row +
+                                            (size_t)(c / 4) * kTileN;
+                        const size_t next = b + stride <= last ? (size_t)(stride * CG) * slot_f4 : 0;
+                        float4 x[4], y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) x[i] = __ldcg(src + (size_t)i * kTileN);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) y[i] = __ldcg(src + next + (size_t)i * kTileN);
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const float4 x = __ldcg(src + (size_t)(c / 4 + i) * kTileN);
-                            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + x.x);
-                            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + x.y);
-                            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + x.z);
-                            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + x.w);
+                            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + x[i].x);
+                            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + x[i].y);
+                            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + x[i].z);
+                            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + x[i].w);
+                        }
+                        if (next) {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + y[i].x);
+                                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + y[i].y);
+                                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + y[i].z);
+                                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + y[i].w);
+                            }
                         }
                     }
                 };
                 // first output of this warp: 32 rows of W, or of W and `up` each (warps w and w + 2)
                 const int64_t nw = ((int64_t)t.n * CG + rank) * rows_a + 32 * (p.up ? quarter & 1 : quarter);
                 if (!p.up) {
-                    for (int c = 16 * set; c < cols; c += 32) {
-                        uint32_t v[16];
-                        sum(c, v);
-                        store16(p, v, t.s0 + c, t.rows - c, nw, lane, stg);
+                    for (int c = 32 * set; c < cols; c += 64) {
+                        uint32_t v[2][16];
+                        sum(c, v[0]);
+                        const bool two = c + 16 < cols;
+                        if (two) sum(c + 16, v[1]);
+                        if (c + 64 >= cols) release();
+                        store32(p, v, two, t.s0 + c, t.rows - c, nw, lane, stg);
                     }
+                    if (32 * set >= cols) release();
                 } else {
                     // Quarter q holds rows of W, quarter q + 2 the same rows of `up`: of every 32 slots the first
                     // computes 16 and gets their `up` sums, the second the other 16 and gets their W sums.
@@ -1096,16 +1182,19 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                             for (int i = 0; i < 16; i++) sts32(mine + (uint32_t)(128 * i), give[i]);
                         }
                         if (ck < cols) sum(ck, keep);
+                        if (c0 + 64 >= cols) release();
                         named_bar_sync(bar, 64);
                         if (ck < cols) {
                             const int valid = t.rows - ck;
+                            uint32_t o[16];
 #pragma unroll
-                            for (int i0 = 0; i0 < 16; i0 += 4) {
+                            for (int i = 0; i < 16; i++) o[i] = lds32(theirs + (uint32_t)(128 * i));
+#pragma unroll
+                            for (int i0 = 0; i0 < 16; i0 += 8) {
                                 if (i0 >= valid) break;
 #pragma unroll
-                                for (int i = i0; i < i0 + 4; i++) {
-                                    const float o = __uint_as_float(lds32(theirs + (uint32_t)(128 * i)));
-                                    const float g = first ? __uint_as_float(keep[i]) : o, u = first ? o : __uint_as_float(keep[i]);
+                                for (int i = i0; i < i0 + 8; i++) {
+                                    const float g = __uint_as_float(first ? keep[i] : o[i]), u = __uint_as_float(first ? o[i] : keep[i]);
                                     keep[i] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * u);
                                 }
                             }
@@ -1113,16 +1202,11 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                         }
                         if (c0 + 64 < cols) named_bar_sync(bar, 64);   // the sums have been read
                     }
+                    if (32 * set >= cols) release();
                 }
                 // the tags are cleared for a replay of this call
                 if (lane == 0)
                     for (int b = worker + stride; b <= last; b += stride) p.flags[(size_t)(b * CG + rank) * kEpiWarps + warp] = 0ull;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2) release_at(in_first(acce + 8 * ra.i));
-                else mbar_arrive(acce + 8 * ra.i);
             }
             ra.advance(p.nacc);
         }
@@ -1454,7 +1538,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1) / CG);
     const uint32_t ctrl = 1024, tab = (uint32_t)(3 * a.E + 1) * 4;
     const uint32_t epi = kEpiWarps * kWarpStage + (p.up ? kExchange : 0);
-    const uint32_t fixed = 1024 + ctrl + epi + ((tab + 15u) & ~15u);
+    const uint32_t tab16 = (tab + 15u) & ~15u, fixed = 1024 + ctrl + epi + tab16 + kListed * (uint32_t)sizeof(Work);
     // tensor memory: accumulators, then rebuilt-A slots (32 columns) or scale columns
     p.acc_w = (uint32_t)(src == kGroupMx8 ? 2 * MG : MG);
     p.sf_slot = src == kGroupMxMx ? 8u + 8u * (uint32_t)mx_row_tiles(MG) : src == kGroupMx8 ? 4u + h.sf_b / 128u : 0u;
@@ -1473,6 +1557,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.ctrl_off = (uint32_t)S * p.stage_bytes;
     p.stg_off = p.ctrl_off + ctrl;
     p.tab_off = p.stg_off + epi;
+    p.work_off = p.tab_off + tab16;
     const size_t smem = (size_t)S * p.stage_bytes + fixed;
 
     Maps m{};

@@ -3,9 +3,12 @@
 //
 // Router.  The choice compares logits only (softmax and sigmoid rise with
 // the logit), by an order-preserving 32-bit key, so it is exact whatever the
-// scores round to.  A warp owns a token: E/32 keys a lane, k rounds of one
-// warp-wide maximum and one minimum over the indices that reach it.  Scores
-// are fp32 with the accurate exponential.
+// scores round to.  A token has G lanes, E/G keys each: 8 lanes (four tokens a
+// warp) up to 256 experts and 8 choices, else a warp.  k rounds take the
+// largest key; a round costs a lane one instruction a key, so few lanes with
+// many keys share its reductions best (16384 tokens, 256 experts, k = 8: XXX us
+// with a warp a token, XXX us with 8 lanes).  Scores are fp32 with the accurate
+// exponential.
 // Slots.  A stable counting sort over at most one CTA per SM: CTA b owns a
 // contiguous run of tokens, counts its choices per expert (k_route_choose),
 // and after all counts are known (k_route_place) adds up the counts of the
@@ -27,7 +30,7 @@ int route_status_take() { return unit_status_take(); }
 
 namespace {
 
-constexpr int kRouteThreads = 1024;   // at most; a single CTA takes a warp per token
+constexpr int kRouteThreads = 1024;   // at most
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kSingle = 512;     // choices up to which one CTA does everything
 
@@ -35,6 +38,7 @@ struct RouteParams {
     const void* logits;
     int64_t T;
     int E, k, score, renorm;
+    int vec;         // rows of four logits a load (E % 4 = 0, aligned)
     float scale;
     int64_t chunk;   // tokens of a CTA
     int32_t* ids;
@@ -49,26 +53,68 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the G lanes of a token.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    for (int d = G / 2; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
     return v;
 }
-
-// Logits of token t, expert 32 i + lane, as fp32 bits (NaN past E); all loads
-// are issued before any is used.
-template <int VPL, bool F32>
-__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, uint32_t (&raw)[VPL]) {
-    if (F32) {
-        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + lane;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) raw[i] = 32 * i + lane < p.E ? __ldg(x + 32 * i) : 0x7FC00000u;
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (G == 32) {
+        return __reduce_max_sync(kFull, v);
     } else {
-        const uint16_t* x = reinterpret_cast<const uint16_t*>(p.logits) + t * p.E + lane;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) raw[i] = 32 * i + lane < p.E ? (uint32_t)__ldg(x + 32 * i) : 0x7FC0u;
+        for (int d = G / 2; d; d >>= 1) {
+            const uint32_t o = __shfl_xor_sync(kFull, v, d);
+            v = v > o ? v : o;
+        }
+        return v;
+    }
+}
+
+// Expert of a lane's key i: four neighbours a load where the lane has so many.
+template <int VPL, int G>
+__device__ __forceinline__ constexpr int expert_of(int i, int lane) {
+    return VPL % 4 ? G * i + lane : 4 * G * (i / 4) + 4 * lane + i % 4;
+}
+
+// Logits of token t as fp32 bits (NaN past E and for the lanes without a
+// token); all loads are issued before any is used.
+template <int VPL, int G, bool F32>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, bool in, int lane, uint32_t (&raw)[VPL]) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(p.logits) + t * p.E;
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p.logits) + t * p.E;
+    if constexpr (VPL % 4 == 0) {
+        if (p.vec) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++) raw[i] <<= 16;
+            for (int i = 0; i < VPL; i += 4) {
+                const int e = expert_of<VPL, G>(i, lane);
+                const bool ok = in && e < p.E;
+                if (F32) {
+                    const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(x + e)) : make_uint4(0x7FC00000u, 0x7FC00000u, 0x7FC00000u, 0x7FC00000u);
+                    raw[i] = v.x;
+                    raw[i + 1] = v.y;
+                    raw[i + 2] = v.z;
+                    raw[i + 3] = v.w;
+                } else {
+                    const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(h + e)) : make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
+                    raw[i] = v.x << 16;
+                    raw[i + 1] = v.x & 0xFFFF0000u;
+                    raw[i + 2] = v.y << 16;
+                    raw[i + 3] = v.y & 0xFFFF0000u;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+        const int e = expert_of<VPL, G>(i, lane);
+        const bool ok = in && e < p.E;
+        if (F32) raw[i] = ok ? __ldg(x + e) : 0x7FC00000u;
+        else raw[i] = ok ? (uint32_t)__ldg(h + e) << 16 : 0x7FC00000u;
     }
 }
 
@@ -82,101 +128,131 @@ __device__ __forceinline__ uint32_t bits_key(uint32_t bits) {
     return k - 0x00800000u > 0xFF800000u - 0x00800000u ? 0u : k < top ? k : top;
 }
 
-// The k largest keys in falling order, equal keys by index: lane j < k ends up
-// with choice j.  k rounds of a maximum over the warp and a minimum over the
-// indices that reach it.
-template <int VPL>
-__device__ __noinline__ uint2 select_exact(const RouteParams& p, int64_t t, int lane) {
+// Where the last choice shares its upper key bits (`prefix`) with keys that
+// were left out: the choices first .. k - 1 of the token are the largest of all
+// keys with that prefix, equal keys by index.  Lane j of the G lanes with first
+// <= j < k ends up with choice j as (expert, key).  `on`: the token needs it
+// (every lane of the warp takes part).
+template <int VPL, int G, int BITS>
+__device__ __noinline__ uint2 select_edge(const RouteParams& p, int64_t t, bool on, int lane, uint32_t prefix, int first) {
     uint32_t key[VPL];
-    load_logits<VPL, true>(p, t, lane, key);
+    load_logits<VPL, G, true>(p, t, on, lane, key);
 #pragma unroll
-    for (int i = 0; i < VPL; i++) key[i] = bits_key(key[i]);
-    uint2 mine = make_uint2(0xFFFFFFFFu, 0);   // (expert, key)
-    for (int j = 0; j < p.k; j++) {
-        uint32_t best = 0, cand = 0xFFFFFFFFu;
+    for (int i = 0; i < VPL; i++) {
+        key[i] = bits_key(key[i]);
+        if ((key[i] >> BITS) != prefix) key[i] = 0;
+    }
+    uint2 mine = make_uint2(0xFFFFFFFFu, 0);
+    for (int j = on ? first : p.k; __any_sync(kFull, j < p.k); j++) {
+        uint32_t best = 0, cand = 0;
 #pragma unroll
         for (int i = 0; i < VPL; i++) best = best > key[i] ? best : key[i];
-        const uint32_t mx = __reduce_max_sync(kFull, best);
-        if (mx == 0) break;
+        const uint32_t mx = group_max<G>(best);
 #pragma unroll
         for (int i = VPL - 1; i >= 0; i--)
-            if (key[i] == mx) cand = (uint32_t)(32 * i + lane);
-        const uint32_t e = __reduce_min_sync(kFull, cand);
+            if (key[i] == mx) cand = (uint32_t)(0x7FFFFFFF - expert_of<VPL, G>(i, lane));   // the lowest index has the largest
+        const uint32_t e = 0x7FFFFFFFu - group_max<G>(cand);
 #pragma unroll
         for (int i = 0; i < VPL; i++)
-            if ((uint32_t)(32 * i + lane) == e) key[i] = 0;
-        if (lane == j) mine = make_uint2(e, mx);
+            if ((uint32_t)expert_of<VPL, G>(i, lane) == e) key[i] = 0;
+        if (lane == j && mx) mine = make_uint2(e, mx);
     }
     return mine;
 }
 
 // One token: lane j < k ends up with choice j (expert id, or -1) and weight.
-// The rounds run on words that join a key's upper 22 bits with the index: one
-// maximum a round, and the word that gave it is unique.  Where two
-// neighbours of the k + 1 largest share those 22 bits and fp32 logits may
-// differ below them (about 1 token in 50), the selection is repeated exactly;
-// the upper 22 bits hold all of a BF16 logit.
-template <int VPL, bool F32>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, const uint32_t (&raw)[VPL], int lane, int& id,
+// The rounds run on words that join a key's upper bits with the index in the
+// lower ones (as many as VPL G experts need): one maximum a round, and the word
+// that gave it is unique.  The upper bits hold all of a BF16 logit.  fp32
+// logits may differ below them: where two neighbours among the choices share
+// them (about 1 token in 200 at 256 experts) the choices are put in order by
+// their full keys; where the last choice shares them with the first one left
+// out (1 in 1500), the keys that share them are selected exactly first.
+template <int VPL, int G, bool F32>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, bool in, uint32_t (&word)[VPL], int lane, int& id,
                                        float& w) {
-    uint32_t word[VPL];
+    constexpr int kBits = VPL * G <= 32 ? 5 : VPL * G <= 64 ? 6 : VPL * G <= 128 ? 7 : VPL * G <= 256 ? 8 : VPL * G <= 512 ? 9 : 10;
+    constexpr uint32_t kLow = (1u << kBits) - 1u;
     uint32_t best = 0;
     float total = 0.0f, m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; i++) word[i] = bits_key(raw[i]);
+    for (int i = 0; i < VPL; i++) word[i] = bits_key(word[i]);
     if (p.score == UW_SCORE_SOFTMAX) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < VPL; i++) top = top > word[i] ? top : word[i];
-        top = __reduce_max_sync(kFull, top);
+        top = group_max<G>(top);
         m = key_logit(top);   // top = 0 (no choice at all): unused
-        if (!p.renorm && top) {   // the denominator over every logit
+        if (!p.renorm) {   // the denominator over every logit
 #pragma unroll
             for (int i = 0; i < VPL; i++)
                 if (word[i]) total += expf(key_logit(word[i]) - m);
-            total = warp_sum(total);
+            total = group_sum<G>(total);
         }
     }
 #pragma unroll
     for (int i = 0; i < VPL; i++) {
-        word[i] = word[i] ? (word[i] & 0xFFFFFC00u) | (uint32_t)(1023 - (32 * i + lane)) : 0u;
+        word[i] = word[i] ? (word[i] & ~kLow) | (kLow - (uint32_t)expert_of<VPL, G>(i, lane)) : 0u;
         best = best > word[i] ? best : word[i];
     }
-    uint32_t got = 0;
-    const int rounds = F32 && p.k < 32 ? p.k + 1 : p.k;   // one more: does the last choice stand out
-    for (int j = 0; j < rounds; j++) {
-        const uint32_t mx = __reduce_max_sync(kFull, best);
-        if (mx == 0) break;
+    uint32_t got = 0, last = 0;
+    bool close = false, edge = false;
+    for (int j = 0;; j++) {
+        const uint32_t mx = group_max<G>(best);
+        // fp32: a word that shares its key bits with the one before (also the first that is not taken)
+        if (F32) edge = j && mx && (mx >> kBits) == (last >> kBits);
+        if (j == p.k) break;
+        close |= edge;
+        last = mx;
         if (lane == j) got = mx;
+        if (!F32 && j + 1 == p.k) break;
         // the largest word below mx: word - mx wraps to the top of the range below it, to its bottom from it up
         uint32_t below = 0;
 #pragma unroll
         for (int i = 0; i < VPL; i++) below = __viaddmax_u32(word[i], 0u - mx, below);
         best = below + mx;
-        best = best < mx ? best : 0u;
+        best = mx && best < mx ? best : 0u;
     }
-    id = got && lane < p.k ? 1023 - (int)(got & 1023u) : -1;
+    id = got ? (int)(kLow - (got & kLow)) : -1;
     uint32_t mine = 0;
-    bool close = false;
-    if (F32) {
-        const uint32_t before = __shfl_up_sync(kFull, got, 1);
-        close = lane && got && (before >> 10) == (got >> 10);
-        // k = 32 has no extra round: what is left over is compared with the last choice
-        const uint32_t last = __shfl_sync(kFull, got, 31);
-        if (p.k == 32) close |= best && (best >> 10) == (last >> 10);
+    if (!F32) {
+        mine = got & ~kLow;
+        if (mine) mine |= mine >> 31 ? 0u : kLow;   // a negative logit's key has its low bits set
+    } else {
+        if (id >= 0) mine = bits_key(__ldg(reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + id));
+        if (__any_sync(kFull, edge)) {
+            // choices above the prefix that the last one shares stand
+            const uint32_t prefix = last >> kBits;
+            const uint32_t above = __ballot_sync(kFull, got && (got >> kBits) > prefix);
+            const int first = __popc(G == 32 ? above : above >> ((threadIdx.x & 31) / G * G) & ((1u << (G % 32)) - 1u));
+            const uint2 x = select_edge<VPL, G, kBits>(p, t, edge, lane, prefix, first);
+            if (edge && lane >= first && lane < p.k) {
+                id = (int)x.x;
+                mine = x.y;
+            }
+        }
+        if (__any_sync(kFull, close || edge)) {   // by (key, index): every lane's place among the choices, then the choice of each place
+            int place = 0, from = lane;
+            for (int i = 0; i < p.k; i++) {
+                const uint32_t k = __shfl_sync(kFull, mine, i, G);
+                const int e = __shfl_sync(kFull, id, i, G);
+                place += k > mine || (k == mine && (uint32_t)e < (uint32_t)id);
+            }
+            for (int i = 0; i < p.k; i++)
+                if (__shfl_sync(kFull, place, i, G) == lane) from = i;
+            // (empty choices, key 0, share a place behind all others: they stay where they are)
+            const uint32_t k = __shfl_sync(kFull, mine, from, G);
+            const int e = __shfl_sync(kFull, id, from, G);
+            if (mine) {
+                mine = k;
+                id = e;
+            }
+        }
     }
-    if (F32 && __any_sync(kFull, close)) {
-        const uint2 x = select_exact<VPL>(p, t, lane);
-        id = (int)x.x;
-        mine = x.y;
-    } else if (id >= 0) {
-        mine = F32 ? bits_key(__ldg(reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + id)) : got & 0xFFFFFC00u;
-    }
-    if (!F32 && mine) mine |= mine >> 31 ? 0u : 0x3FFu;   // a negative logit's key has its low bits set
     const float x = key_logit(mine);
     float s = 0.0f;
     if (mine) s = p.score == UW_SCORE_SOFTMAX ? expf(x - m) : 1.0f / (1.0f + expf(-x));
-    if (p.renorm) total = warp_sum(s);
+    if (p.renorm) total = group_sum<G>(s);
     if (p.score == UW_SCORE_SOFTMAX || p.renorm) s = total > 0.0f ? s / total : 0.0f;
     w = mine ? s * p.scale : 0.0f;
 }
@@ -298,7 +374,7 @@ __device__ __forceinline__ void place(const RouteParams& p, int32_t* sm, int cta
         p.rows[i] = -1;
 }
 
-template <int VPL, bool F32>
+template <int VPL, int G, bool F32>
 __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParams p) {
     extern __shared__ int32_t sm[];
     int32_t* counts = sm;
@@ -312,20 +388,22 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_choose(const RouteParam
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     const int64_t t1 = t0 + p.chunk < p.T ? t0 + p.chunk : p.T;
-    uint32_t raw[VPL], next[VPL];
-    if (t0 + warp < t1) load_logits<VPL, F32>(p, t0 + warp, lane, next);
-    for (int64_t t = t0 + warp; t < t1; t += warps) {
-#pragma unroll
-        for (int i = 0; i < VPL; i++) raw[i] = next[i];
-        if (t + warps < t1) load_logits<VPL, F32>(p, t + warps, lane, next);   // the next token's, meanwhile
+    // a warp takes 32 / G tokens at a time
+    constexpr int kTok = 32 / G;
+    const int gl = lane % G;
+    for (int64_t tw = t0 + (int64_t)warp * kTok; tw < t1; tw += (int64_t)warps * kTok) {
+        const int64_t t = tw + lane / G;
+        const bool in = t < t1;
+        uint32_t raw[VPL];
+        load_logits<VPL, G, F32>(p, t, in, gl, raw);
         int id;
         float w;
-        choose<VPL, F32>(p, t, raw, lane, id, w);
-        if (lane < p.k) {
-            p.ids[t * p.k + lane] = id;
-            p.weights[t * p.k + lane] = w;
+        choose<VPL, G, F32>(p, t, in, raw, gl, id, w);
+        if (in && gl < p.k) {
+            p.ids[t * p.k + gl] = id;
+            p.weights[t * p.k + gl] = w;
             if (id >= 0) atomicAdd(&counts[id], 1);
-            if (single) ids[t * p.k + lane] = id;
+            if (single) ids[t * p.k + gl] = id;
         }
     }
     __syncthreads();
@@ -357,14 +435,21 @@ cudaError_t launch_pdl(void (*kern)(const P), int64_t grid, int threads, size_t 
 }
 
 typedef void (*RouteKernel)(const RouteParams);
+// (a warp a token while an SM has fewer than 16 tokens: then the rounds' latency counts)
+bool eight_lanes(int64_t T, int E, int k, int ctas) { return E <= 256 && k <= 8 && T >= 16 * (int64_t)ctas && ctas > 1; }
 template <bool F32>
-RouteKernel route_kernel(int E) {
-    return E <= 32    ? k_route_choose<1, F32>
-           : E <= 64  ? k_route_choose<2, F32>
-           : E <= 128 ? k_route_choose<4, F32>
-           : E <= 256 ? k_route_choose<8, F32>
-           : E <= 512 ? k_route_choose<16, F32>
-                      : k_route_choose<32, F32>;
+RouteKernel route_kernel(int E, bool eight) {
+    if (eight)
+        return E <= 32    ? k_route_choose<4, 8, F32>
+               : E <= 64  ? k_route_choose<8, 8, F32>
+               : E <= 128 ? k_route_choose<16, 8, F32>
+                          : k_route_choose<32, 8, F32>;
+    return E <= 32    ? k_route_choose<1, 32, F32>
+           : E <= 64  ? k_route_choose<2, 32, F32>
+           : E <= 128 ? k_route_choose<4, 32, F32>
+           : E <= 256 ? k_route_choose<8, 32, F32>
+           : E <= 512 ? k_route_choose<16, 32, F32>
+                      : k_route_choose<32, 32, F32>;
 }
 
 // ---------------------------------------------------------------- combination
@@ -510,6 +595,7 @@ cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k
     p.k = k;
     p.score = score;
     p.renorm = renorm;
+    p.vec = E % 4 == 0 && ((uintptr_t)logits & (in_f32 ? 15 : 7)) == 0;
     p.scale = scale;
     const int ctas = route_blocks(T, k);
     p.chunk = (T + ctas - 1) / ctas;
@@ -520,13 +606,14 @@ cudaError_t launch_route(const void* logits, int in_f32, int64_t T, int E, int k
     p.pos = pos;
     p.hist = hist;
     // a single CTA: a warp per token, 4 at least
+    const bool eight = eight_lanes(T, E, k, ctas);
     int threads = kRouteThreads;
     if (ctas == 1) {
         const int64_t want = 32 * (T > 4 ? T : 4);
         threads = (int)(want < kRouteThreads ? want : kRouteThreads);
     }
     const size_t smem = (size_t)(2 * E + 1 + threads / 32 * E) * 4;
-    const RouteKernel choose_k = in_f32 ? route_kernel<true>(E) : route_kernel<false>(E);
+    const RouteKernel choose_k = in_f32 ? route_kernel<true>(E, eight) : route_kernel<false>(E, eight);
     const size_t smem_c = (size_t)E * 4 + (ctas == 1 ? kSingle * 4 + smem : 0);
     cudaError_t e = smem_c > 48 * 1024 ? set_smem_attr((const void*)choose_k, (int)smem_c) : cudaSuccess;
     if (e == cudaSuccess && smem > 48 * 1024) e = set_smem_attr((const void*)k_route_place, (int)smem);
