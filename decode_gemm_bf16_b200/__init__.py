@@ -579,14 +579,14 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
 def _output(out, shape, out_f32: bool, like: torch.Tensor) -> torch.Tensor:
     dtype = torch.float32 if out_f32 else torch.bfloat16
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
     return _need(out, "out", (dtype,), shape, like.device)
 
 
-def _scratch(ws, nbytes: int, device: torch.device) -> torch.Tensor:
+def _scratch(ws, nbytes: int, like: torch.Tensor) -> torch.Tensor:
     if ws is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    return _need(ws, "ws", _U8, device=device)
+        return torch.empty(nbytes or 256, dtype=torch.uint8, device=like.device)
+    return _need(ws, "ws", _U8, device=like.device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -688,8 +688,8 @@ def _mx_gemm(handle, X, W, mx, out, out_f32, ws):
     M, N = X.shape[0], W.rows
     if not mx:
         X = _rows(X)
-    out = _output(out, (M, N), out_f32, W.codes)
-    ws = _scratch(ws, _mx_gemm_bytes(W.device.index, M, N, W.K, mx), W.device)
+    out = _output(out, (M, N), out_f32, W.codes if mx else X)
+    ws = _scratch(ws, _mx_gemm_bytes(W.device.index, M, N, W.K, mx), W.codes)
     _check(lib().uw_mx_gemm(None if mx else X.data_ptr(), ctypes.byref(X._desc) if mx else None, M, ctypes.byref(W._desc),
                             out.data_ptr(), 1 if out_f32 else 0, ws.data_ptr(), ws.numel(), handle), "uw_mx_gemm")
     return out
@@ -738,7 +738,7 @@ def _route(handle, logits, k, score, renorm, scale, ws):
     weights = torch.empty_like(ids, dtype=torch.float32)
     offsets, rows = logits.new_empty(E + 1, dtype=i32), logits.new_empty(T * k, dtype=i32)
     if ws is not None or need:
-        ws = _scratch(ws, need, logits.device)
+        ws = _scratch(ws, need, logits)
     _check(lib().uw_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, T, E, k, score, 1 if renorm else 0, scale,
                           ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
                           None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), handle), "uw_route")
@@ -809,7 +809,7 @@ def _gemm_grouped(handle, X, W, offsets, rows, up, shape, out, out_f32, ws):
     out = _output(out, (slots, N), out_f32, X)
     a = _group_args(X.data_ptr(), X.shape[0], None if rows is None else rows.data_ptr(), slots, offsets.data_ptr(), E, N, K, W, up,
                     out.data_ptr(), 1 if out_f32 else 0)
-    ws = _scratch(ws, _group_bytes(a), X.device)
+    ws = _scratch(ws, _group_bytes(a), X)
     a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
     _check(lib().uw_gemm_grouped(ctypes.byref(a), handle), "uw_gemm_grouped")
     return out
