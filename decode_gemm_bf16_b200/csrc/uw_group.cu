@@ -132,15 +132,15 @@ struct Plan {
     const int32_t* cum;      // [E + 1] tiles before each expert
     const int32_t* begin;    // [E] first slot
     const int32_t* count;    // [E] slots
-    int64_t tiles, whole;    // tiles; tiles dealt out whole (the first ones)
-    int64_t units;           // k steps of the cut tiles (contiguous ranges)
-    int ps;                  // of the P workers, those that share them
-    int P;
-    int parts, rest;
+    uint32_t whole;          // tiles dealt out whole (the first ones)
+    uint32_t units;          // k steps of the cut tiles (contiguous ranges; the host checks that units * P < 2^32)
+    uint32_t ps;             // of the P workers, those that share them
+    uint32_t P;
+    uint32_t parts, rest;
 };
 
 struct Seg {
-    int64_t tile;
+    uint32_t tile;
     int kt0, kt1;
 };
 
@@ -161,37 +161,36 @@ struct Tile {
 };
 
 // Units of worker b's range start here; owner of a unit.
-__device__ __forceinline__ int64_t unit_begin(int64_t b, const Plan& pl) { return b * pl.units / pl.ps; }
-__device__ __forceinline__ int unit_owner(int64_t u, const Plan& pl) { return (int)(((u + 1) * pl.ps - 1) / pl.units); }
+__device__ __forceinline__ uint32_t unit_begin(uint32_t b, const Plan& pl) { return b * pl.units / pl.ps; }
+__device__ __forceinline__ uint32_t unit_owner(uint32_t u, const Plan& pl) { return ((u + 1) * pl.ps - 1) / pl.units; }
 
 // Segment i of worker b: its range or part of the cut tiles first (joining them
 // then overlaps the whole tiles), then its whole tiles.
-__device__ __forceinline__ bool segment(const Plan& pl, int b, int i, int kt, Seg& s) {
+__device__ __forceinline__ bool segment(const Plan& pl, uint32_t b, uint32_t i, uint32_t kt, Seg& s) {
     if (b < pl.ps) {
-        const int64_t u0 = unit_begin(b, pl), ue = unit_begin(b + 1, pl);
-        const int64_t t0 = u0 / kt;
-        const int n = ue > u0 ? (int)((ue - 1) / kt - t0) + 1 : 0;
+        const uint32_t u0 = unit_begin(b, pl), ue = unit_begin(b + 1, pl), t0 = u0 / kt;
+        const uint32_t n = ue > u0 ? (ue - 1) / kt - t0 + 1 : 0;
         if (i < n) {
-            const int64_t first = i ? (t0 + i) * kt : u0, end = (t0 + i + 1) * kt < ue ? (t0 + i + 1) * kt : ue;
+            const uint32_t tile0 = (t0 + i) * kt, end = tile0 + kt < ue ? tile0 + kt : ue;
             s.tile = pl.whole + t0 + i;
-            s.kt0 = (int)(first - (t0 + i) * kt);
-            s.kt1 = (int)(end - (t0 + i) * kt);
+            s.kt0 = i ? 0 : (int)(u0 - tile0);
+            s.kt1 = (int)(end - tile0);
             return true;
         }
         i -= n;
     } else if (b < pl.parts * pl.rest) {
         if (i == 0) {
-            const int part = b / pl.rest;
-            s.tile = pl.whole + b % pl.rest;
-            s.kt0 = part * kt / pl.parts;
-            s.kt1 = (part + 1) * kt / pl.parts;
+            const uint32_t part = b / pl.rest;
+            s.tile = pl.whole + b - part * pl.rest;
+            s.kt0 = (int)(part * kt / pl.parts);
+            s.kt1 = (int)((part + 1) * kt / pl.parts);
             return true;
         }
         i--;
     }
-    s.tile = b + (int64_t)i * pl.P;
+    s.tile = b + i * pl.P;
     s.kt0 = 0;
-    s.kt1 = kt;
+    s.kt1 = (int)kt;
     return s.tile < pl.whole;
 }
 
@@ -204,7 +203,8 @@ struct Work {
     Tile tile;
 };
 
-__device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int64_t tile) {
+__device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, uint32_t utile) {
+    const int tile = (int)utile;   // below 2^31
     int lo = 0, hi = p.E;   // last expert with cum[e] <= tile (experts without tiles are passed over)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -212,7 +212,7 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, int
     }
     const int c = pl.count[lo];
     const int mt = (c + p.MG - 1) / p.MG;
-    int l = (int)(tile - pl.cum[lo]);
+    int l = tile - pl.cum[lo];
     const int band = l / (kBand * p.n_tiles);
     l -= band * kBand * p.n_tiles;
     const int nb = mt - band * kBand < kBand ? mt - band * kBand : kBand;
@@ -238,7 +238,7 @@ struct Walk {
             i++;
             return t.rows > 0;
         }
-        if (!segment(pl, worker, i, p.kt, s)) return false;
+        if (!segment(pl, (uint32_t)worker, (uint32_t)i, (uint32_t)p.kt, s)) return false;
         i++;
         t = locate(p, pl, s.tile);
         return true;
@@ -745,23 +745,25 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     // and half of the tile's X; the first issues the MMAs of both.
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)(blockIdx.x / CG);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.S; s++) {
-            mbar_init(joins + 8 * s, 1);
-            mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);
-            mbar_init(mixed + 8 * s, CG);
+    if (warp == 0) {   // a lane a barrier of each kind
+        if (lane < p.S) {
+            mbar_init(full + 8 * lane, 1);
+            mbar_init(empty + 8 * lane, 1);
+            mbar_init(joins + 8 * lane, 1);
+            mbar_init(mixed + 8 * lane, CG);
         }
-        for (int t = 0; t < p.T; t++) {
-            mbar_init(recon + 8 * t, kRebuildWarps);
-            mbar_init(tfree + 8 * t, 1);
+        if (kRe && lane < p.T) {
+            mbar_init(recon + 8 * lane, kRebuildWarps);
+            mbar_init(tfree + 8 * lane, 1);
         }
-        for (int a = 0; a < 2; a++) {
-            mbar_init(accf + 8 * a, 1);
-            mbar_init(acce + 8 * a, kEpiWarps * CG);
+        if (lane < 2) {
+            mbar_init(accf + 8 * lane, 1);
+            mbar_init(acce + 8 * lane, kEpiWarps * CG);
         }
-        mbar_init(fin, 1);
-        *abort_flag = 0;
+        if (lane == 0) {
+            mbar_init(fin, 1);
+            *abort_flag = 0;
+        }
         fence_barrier_init();
     }
     if (warp == kMma) pair_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
@@ -784,31 +786,32 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     pl.cum = cum;
     pl.begin = begin;
     pl.count = count;
-    pl.tiles = cum[p.E];
     {
-        const int64_t P = gridDim.x / CG, rounds = pl.tiles / P, rest = pl.tiles % P;
-        pl.P = (int)P;
+        const uint32_t tiles = (uint32_t)cum[p.E], P = gridDim.x / CG, rounds = tiles / P, rest = tiles - rounds * P;
+        pl.P = P;
         pl.units = pl.ps = pl.parts = pl.rest = 0;
-        pl.whole = pl.tiles;
+        pl.whole = tiles;
         if (p.parts) {
-            const int64_t most = rest ? P / rest : 0, parts = most < p.kt / 2 ? most : p.kt / 2;   // two k steps at least
-            if (parts > 1) {
-                pl.parts = (int)parts;
-                pl.rest = (int)rest;
-                pl.whole = pl.tiles - rest;
+            // joining parts takes about 7 us of the first one's time: worth it when that is less than the k steps
+            // (2 cycles a column and step) that the others take off it
+            const uint32_t parts = rest ? P / rest : 0;
+            if (parts > 1 && (uint64_t)p.kt * p.acc_w * (parts - 1) > 7000ull * parts) {
+                pl.parts = parts;
+                pl.rest = rest;
+                pl.whole = tiles - rest;
             }
         } else if (rest) {
             pl.whole = rounds > 1 ? (rounds - 1) * P : 0;
-            pl.units = (pl.tiles - pl.whole) * p.kt;
+            pl.units = (tiles - pl.whole) * (uint32_t)p.kt;
             // a range shorter than two k steps costs more to join than it saves
-            const int64_t most = (pl.units + 1) / 2;
-            pl.ps = (int)(P < most ? P : most);
+            const uint32_t most = (pl.units + 1) / 2;
+            pl.ps = P < most ? P : most;
         }
     }
     Work* work = reinterpret_cast<Work*>(smem + p.work_off);
     for (int i = threadIdx.x; i < kListed; i += blockDim.x) {
         Work w;
-        if (segment(pl, worker, i, p.kt, w.seg)) w.tile = locate(p, pl, w.seg.tile);
+        if (segment(pl, (uint32_t)worker, (uint32_t)i, (uint32_t)p.kt, w.seg)) w.tile = locate(p, pl, w.seg.tile);
         else w.tile.rows = 0;
         work[i] = w;
     }
@@ -1069,9 +1072,9 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             const uint32_t lo = (uint32_t)(mma_n<SRC, CG>(t.rows) / 2);   // split rows: first lo column
             const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
             // the tile's other ranges, in k order: workers worker + stride, ... up to `last`
-            const int stride = pl.parts ? pl.rest : 1;
+            const int stride = pl.parts ? (int)pl.rest : 1;
             int last = worker;
-            if (joins) last = pl.parts ? worker + (pl.parts - 1) * stride : unit_owner((sg.tile - pl.whole + 1) * p.kt - 1, pl);
+            if (joins) last = pl.parts ? worker + (int)(pl.parts - 1) * stride : (int)unit_owner((sg.tile - pl.whole + 1) * (uint32_t)p.kt - 1, pl);
             bool good = true;
             for (int b = worker + stride; good && b <= last; b += stride)
                 good = wait_tag(p.flags + (size_t)(b * CG + rank) * kEpiWarps + warp, p.epoch, p.timeout, abort_flag);
@@ -1115,9 +1118,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
                 }
-                release();
-                __threadfence();
-                __syncwarp();
+                release();   // (synchronises the warp: the tag's release covers every lane's stores)
                 if (lane == 0)
                     asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)blockIdx.x * kEpiWarps + warp),
                                  "l"(p.epoch)
@@ -1490,7 +1491,8 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     const Shape h = shape_of(src, a.slots, a.E, a.N, a.K, a.up != nullptr, a.rows != nullptr);
     const int MG = h.MG, P = num_sms();
     const int64_t max_tiles = h.m_tiles * (int64_t)h.n_tiles;
-    if (max_tiles > 0x7FFFFFFF) { *st = UW_ERR_SHAPE; return cudaSuccess; }
+    // 31-bit tiles; (k steps of two rounds) * CTAs in 32 bits
+    if (max_tiles > 0x7FFFFFFF || 2 * (int64_t)P * P * h.kt >= (int64_t(1) << 32)) { *st = UW_ERR_SHAPE; return cudaSuccess; }
     if (!a.ws || a.ws_bytes < h.bytes()) { *st = UW_ERR_WORKSPACE; return cudaSuccess; }
     uint8_t* prep = (uint8_t*)a.ws + h.partial + h.flags;
     GroupParams p{};
