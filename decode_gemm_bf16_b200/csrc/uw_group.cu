@@ -922,7 +922,8 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             for (int kt = sg.kt0; kt < sg.kt1; kt++) {
                 if (kRe && !wait_one(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
                 if (SRC == kGroupMx8 && p.up && !wait_pair<CG>(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (!wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
+                // (one CTA: joined scales come after everything else of the stage)
+                if (!(SRC == kGroupMx8 && CG == 1 && p.up) && !wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (kScaled) {
                     // scales of the stage, 4 columns per 512 bytes: weights, then rows

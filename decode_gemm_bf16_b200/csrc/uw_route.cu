@@ -19,8 +19,9 @@
 // With few choices one CTA does both parts in a single launch.
 //
 // Combination.  Y[t] = sum_j w[t,j] Z[pos[t,j]]: bound by reading T k N and
-// writing T N values once; a thread owns 8 columns of one token and has its
-// first eight choices' rows in flight before it adds.
+// writing T N values once.  A warp owns 256 columns of one token at a time, 8 a
+// lane; lane j holds choice j, and the next item's choices are loaded before
+// the eight rows in flight are added.
 #include "uw_device.cuh"
 #include "uw_internal.h"
 
@@ -465,7 +466,7 @@ struct CombineParams {
     int64_t T;
     int k;
     int64_t N;
-    int64_t groups;   // column groups of 8
+    int64_t groups;   // column groups of 256
     void* Y;
 };
 
@@ -516,35 +517,51 @@ template <bool IN32, bool OUT32>
 __global__ void __launch_bounds__(kCombineThreads, IN32 ? 2 : 4) k_combine(const CombineParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
-    if (i >= p.T * p.groups) return;
-    const int64_t t = i / p.groups, c = (i - t * p.groups) * kCombineCols;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kCombineThreads / 32), items = p.T * p.groups;
+    int64_t i = (int64_t)blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
     const bool vec = p.N % 8 == 0;
-    const int n = p.N - c < 8 ? (int)(p.N - c) : 8;
+    bool wrong = false;
+    int32_t s_next = -1;
+    float w_next = 0.0f;
+    auto choice = [&](int64_t item) {   // lane j: choice j of the item's token
+        s_next = -1;
+        w_next = 0.0f;
+        if (item < items && lane < p.k) {
+            const int64_t at = item / p.groups * p.k + lane;
+            s_next = __ldg(p.pos + at);
+            w_next = __ldg(p.weights + at);
+            if (s_next >= p.slots) {
+                wrong = true;
+                s_next = -1;
+            }
+        }
+    };
+    choice(i);
+    for (; i < items; i += warps) {
+    const int64_t t = i / p.groups, c = (i - t * p.groups) * (32 * kCombineCols) + lane * kCombineCols;
+    const int n = p.N - c < 8 ? (int)(p.N - c) : 8;   // columns of this lane (none or less than none: past the row)
+    const int32_t s_mine = s_next;
+    const float w_mine = w_next;
     float acc[8] = {};
     for (int j0 = 0; j0 < p.k; j0 += kCombineAhead) {
-        // all positions, then all rows: nothing in between that the loads would wait for
         Cols<IN32> z[kCombineAhead];
-        float w[kCombineAhead];
-        int32_t s[kCombineAhead];
 #pragma unroll
         for (int j = 0; j < kCombineAhead; j++) {
-            s[j] = j0 + j < p.k ? __ldg(p.pos + t * p.k + j0 + j) : -1;
-            w[j] = j0 + j < p.k ? __ldg(p.weights + t * p.k + j0 + j) : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kCombineAhead; j++) {
+            const int32_t s = j0 + j < p.k ? __shfl_sync(kFull, s_mine, j0 + j) : -1;
             z[j].a = z[j].b = make_uint4(0, 0, 0, 0);
-            if (s[j] >= 0 && s[j] < p.slots) load_cols<IN32>(p.Z, s[j] * p.N + c, n, vec, z[j]);
+            if (s >= 0 && n > 0) load_cols<IN32>(p.Z, s * p.N + c, n, vec, z[j]);
         }
-        bool wrong = false;
+        if (j0 == 0) choice(i + warps);   // meanwhile
 #pragma unroll
         for (int j = 0; j < kCombineAhead; j++) {
-            wrong |= s[j] >= p.slots;
-            add_cols<IN32>(z[j], s[j] < 0 || s[j] >= p.slots ? 0.0f : w[j], acc);
+            if (j0 + j >= p.k) break;
+            const int32_t s = __shfl_sync(kFull, s_mine, j0 + j);
+            const float w = __shfl_sync(kFull, w_mine, j0 + j);
+            add_cols<IN32>(z[j], s < 0 ? 0.0f : w, acc);
         }
-        if (wrong) raise_status(UW_ERR_DEVICE);
     }
+    if (n <= 0) continue;
     const int64_t at = t * p.N + c;
     if (OUT32) {
         float* y = reinterpret_cast<float*>(p.Y) + at;
@@ -573,6 +590,8 @@ __global__ void __launch_bounds__(kCombineThreads, IN32 ? 2 : 4) k_combine(const
                 if (q < n) y[q] = __float2bfloat16_rn(acc[q]);
         }
     }
+    }
+    if (wrong) raise_status(UW_ERR_DEVICE);
 }
 
 }  // namespace
@@ -633,9 +652,10 @@ cudaError_t launch_combine(const void* Z, int in_f32, int64_t slots, const int32
     p.T = T;
     p.k = k;
     p.N = N;
-    p.groups = (N + kCombineCols - 1) / kCombineCols;
+    p.groups = (N + 32 * kCombineCols - 1) / (32 * kCombineCols);
     p.Y = Y;
-    const int64_t grid = (T * p.groups + kCombineThreads - 1) / kCombineThreads;
+    const int64_t ctas = (T * p.groups + kCombineThreads / 32 - 1) / (kCombineThreads / 32), most = (int64_t)num_sms() * (in_f32 ? 2 : 4);
+    const int64_t grid = ctas < most ? ctas : most;
     void (*kern)(const CombineParams) = in_f32 ? (out_f32 ? k_combine<true, true> : k_combine<true, false>)
                                                : (out_f32 ? k_combine<false, true> : k_combine<false, false>);
     return launch_pdl<CombineParams>(kern, grid, kCombineThreads, 0, s, p);

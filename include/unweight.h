@@ -420,8 +420,9 @@ uw_status uw_mx_dequantize(const uw_mx_matrix* m, void* out, int out_f32, void* 
  *     BF16 on chip, exactly wherever BF16 holds the value.
  *   X_mx: MXFP4 [M,K] (batch 1; M = its rows): block-scaled 4-bit products.
  * Y: device [M,N], BF16 or float32 (out_f32), 16-byte aligned.  M = 0 is a
- * no-op.  workspace: 256-byte aligned, any contents, owned by the call until
- * it completes (a captured call owns it whenever its graph runs). */
+ * no-op.  K above about 6 million: UW_ERR_SHAPE.  workspace: 256-byte aligned,
+ * any contents, owned by the call until it completes (a captured call owns it
+ * whenever its graph runs). */
 uw_status uw_mx_gemm_workspace(int64_t M, int64_t N, int64_t K, int x_mx, size_t* bytes);
 
 uw_status uw_mx_gemm(const uint16_t* X, const uw_mx_matrix* X_mx, int64_t M, const uw_mx_matrix* W, void* Y, int out_f32,
@@ -471,7 +472,8 @@ uw_status uw_route(const void* logits, int in_f32, int64_t T, int E, int k, int 
  *     in a group raises it too; that slot's outputs are unspecified.  No
  *     access leaves the buffers.
  *   W / up: device BF16 [E, N, K], or W_mx / up_mx: MXFP4 (batch E, rows N;
- *     values of X as in uw_mx_gemm).  Both of one kind.  E <= 1024, E * N <= 2^31 - 256.
+ *     values of X as in uw_mx_gemm).  Both of one kind.  E <= 1024, E * N <= 2^31 - 256,
+ *     K up to about 6 million.
  *   Y: device [slots, N], BF16 or float32 (out_f32), 16-byte aligned.
  *   workspace: 256-byte aligned, any contents, owned by the call until it
  *     completes (a captured call owns it whenever its graph runs). */
