@@ -6,8 +6,8 @@
 // scores round to.  A token has G lanes, E/G keys each: 8 lanes (four tokens a
 // warp) up to 256 experts and 8 choices, else a warp.  k rounds take the
 // largest key; a round costs a lane one instruction a key, so few lanes with
-// many keys share its reductions best (16384 tokens, 256 experts, k = 8: XXX us
-// with a warp a token, XXX us with 8 lanes).  Scores are fp32 with the accurate
+// many keys share its reductions best (16384 tokens, 256 experts, k = 8, BF16:
+// 22.9 us with a warp a token, 17.7 us with 8 lanes).  Scores are fp32 with the accurate
 // exponential.
 // Slots.  A stable counting sort over at most one CTA per SM: CTA b owns a
 // contiguous run of tokens, counts its choices per expert (k_route_choose),

@@ -500,3 +500,127 @@ def test_full_size_experts(mx):
     for sizes in ([2, 0, 5, 1], [700, 3, 0, 321]):
         X, W, off, rows, ref, tol = _grouped_case(sizes, N, K, mx, True, True, T=64)
         U.check(uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1]), ref, tol)
+
+
+# ---------------------------------------------------------------- drawn shapes, large ones, calls at once
+@pytest.mark.parametrize("seed", range(24))
+def test_grouped_drawn(seed):
+    rng = np.random.default_rng(seed)
+    E = int(2 ** rng.uniform(0, 6.5))
+    R = int(2 ** rng.uniform(0, 10.5))
+    p = np.arange(1, E + 1) ** -rng.uniform(0, 2)
+    sizes = rng.multinomial(R, p / p.sum()).tolist()
+    N, K = int(2 ** rng.uniform(0, 9.5)), 64 * int(rng.integers(1, 20))
+    mx, up, gather = (bool(v) for v in rng.integers(0, 2, 3))
+    X, W, off, rows, ref, tol = _grouped_case(sizes, N, K, mx, up, gather, seed=seed)
+    f32 = bool(rng.integers(0, 2))
+    U.check(uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1] if up else None, out_f32=f32), ref, tol)
+
+
+@pytest.mark.parametrize("E", [257, 1024])
+@pytest.mark.parametrize("mx", [False, True])
+def test_grouped_many_experts(E, mx):
+    sizes = [(e * 7919) % 5 if e % 3 else 0 for e in range(E)]
+    X, W, off, rows, ref, tol = _grouped_case(sizes, 72, 128, mx, True, True)
+    U.check(uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1]), ref, tol)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("R", [200, 2000, 9000])
+def test_grouped_rounds_and_cut_tiles(mx, up, R):
+    """Every way of sharing out tiles: fewer than workers, whole rounds, a rest cut in parts (long K)."""
+    for N, K in ((1000, 4096), (2304, 1024)):
+        X, W, off, rows, ref, tol = _grouped_case([R // 2, 0, R - R // 2], N, K, mx, up, False)
+        U.check(uw.uw_gemm_grouped(X, W[0], off, up=W[1] if up else None), ref, tol)
+
+
+def test_grouped_outputs_past_32_bits():
+    """2.3e9 outputs: the last slots' addresses pass 2^31 elements and 2^32 bytes."""
+    R, N, K = 70000, 32768, 64
+    X = _bf16(R, K, seed=1)
+    W = _bf16(2, N, K, seed=2, scale=0.1)
+    off = torch.tensor([0, 100, R], dtype=torch.int32, device="cuda")
+    y = uw.uw_gemm_grouped(X, W, off)
+    for lo, hi, e in ((0, 100, 0), (100, 300, 1), (R - 130, R, 1)):
+        ref = X[lo:hi].double() @ W[e].double().T
+        U.check(y[lo:hi], ref, U.product_tolerance(X[lo:hi].double().abs() @ W[e].double().abs().T, K))
+    z = uw.uw_combine(y, torch.tensor([[R - 1, 5], [-1, R - 2]], dtype=torch.int32, device="cuda"),
+                      torch.tensor([[0.5, 0.25], [9.0, 1.0]], device="cuda"), out_f32=True)
+    want = torch.stack([0.5 * y[R - 1].double() + 0.25 * y[5].double(), y[R - 2].double()])
+    U.check(z, want, 2.0 ** -22 * (y[R - 1].double().abs() + y[5].double().abs() + y[R - 2].double().abs()).expand(2, N))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_grouped_weights_past_32_bits(mx):
+    """17 experts of 14336 x 16384 (4e9 weights): the last ones' addresses pass 2^31 elements and 2^32 bytes."""
+    E, N, K = 17, 14336, 16384
+    W = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+    g = _gen(5)
+    for e in range(E):
+        W[e] = torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16) * 0.01
+    off = torch.tensor([0] + [3] * 15 + [5, 8], dtype=torch.int32, device="cuda")
+    X = _bf16(8, K, seed=3)
+    Wm = uw.uw_mx_quantize(W) if mx else W
+    y = uw.uw_gemm_grouped(X, Wm, off)
+    for lo, hi, e in ((0, 3, 0), (3, 5, 15), (5, 8, 16)):
+        w = (uw.uw_mx_dequantize(uw.uw_mx_quantize(W[e])) if mx else W[e]).double()
+        x = X[lo:hi].double()
+        tol = U.product_tolerance(x.abs() @ w.abs().T, K) + (U.split_tolerance(x, w) if mx else 0)
+        U.check(y[lo:hi], x @ w.T, tol)
+
+
+def test_calls_at_once_on_two_streams():
+    """Small and large tiles, 4-bit and BF16, on two streams at the same time: each as alone."""
+    cases = [_grouped_case([3, 0, 20], 300, 512, True, True, True, seed=1), _grouped_case([700, 300, 5], 500, 1024, False, False, True, seed=2),
+             _grouped_case([150, 300], 384, 2048, True, False, False, seed=3), _grouped_case([1, 2], 2000, 4096, False, True, False, seed=4)]
+    x = _bf16(333, 512, seed=9)
+    call = lambda c: uw.uw_gemm_grouped(c[0], c[1][0], c[2], rows=c[3], up=c[1][1] if len(c[1]) > 1 else None)  # noqa: E731
+    alone = [call(c) for c in cases]
+    route = uw.uw_route(x.float(), 4)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for i in range(12):
+        for s in (0, 1):
+            with torch.cuda.stream(streams[s]):
+                got[s].append((call(cases[(i + 2 * s) % 4]), uw.uw_route(x.float(), 4), uw.uw_mx_dequantize(uw.uw_mx_quantize(x))))
+    torch.cuda.synchronize()
+    for s in (0, 1):
+        for i, (y, r, q) in enumerate(got[s]):
+            assert torch.equal(y, alone[(i + 2 * s) % 4])
+            assert all(torch.equal(a, b) for a, b in zip(r, route))
+            assert torch.equal(q, got[0][0][2])
+
+
+def test_python_refusals():
+    X, W, off, rows, _, _ = _grouped_case([3, 2], 64, 128, False, True, True)
+    M = uw.uw_mx_quantize(W[0])
+    bad = [lambda: uw.uw_gemm_grouped(X.float(), W[0], off, rows=rows),
+           lambda: uw.uw_gemm_grouped(X[:, :64], W[0], off, rows=rows),
+           lambda: uw.uw_gemm_grouped(X, W[0], off[:2], rows=rows),
+           lambda: uw.uw_gemm_grouped(X, W[0], off.long(), rows=rows),
+           lambda: uw.uw_gemm_grouped(X, W[0], off.cpu(), rows=rows),
+           lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows.view(1, -1)),
+           lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=M),
+           lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1][:, :32]),
+           lambda: uw.uw_gemm_grouped(X, W[0].transpose(1, 2), off, rows=rows),
+           lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows, out=torch.empty(5, 63, dtype=torch.bfloat16, device="cuda")),
+           lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows, out=torch.empty(5, 64, device="cuda")),
+           lambda: uw.uw_mx_gemm(X, uw.uw_mx_quantize(W[0][0, :, :64].contiguous())),
+           lambda: uw.uw_mx_quantize(X[0]), lambda: uw.uw_mx_quantize(X.half()),
+           lambda: uw.MxMatrix(M.codes, M.scales[:-1]), lambda: uw.MxMatrix(M.codes.float(), M.scales),
+           lambda: uw.uw_route(X, 2, score="relu"), lambda: uw.uw_route(X[0], 2), lambda: uw.uw_route(X.half(), 2),
+           lambda: uw.uw_combine(X, off, off), lambda: uw.uw_combine(X, rows.view(-1, 1), rows.view(-1, 1)),
+           lambda: uw.uw_combine(X[0], rows.view(-1, 1), rows.view(-1, 1).float())]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for f, status in ((lambda: uw.uw_gemm_grouped(X, W[0], off, rows=rows, ws=small), 5), (lambda: uw.uw_mx_gemm(X, uw.uw_mx_quantize(W[0][0]), ws=small), 5),
+                      (lambda: uw.uw_route(X, 40), 2), (lambda: uw.uw_route(X, 0), 1), (lambda: uw.uw_mx_quantize(_bf16(4, 96)), 2),
+                      (lambda: uw.uw_mx_gemm(X, M), 2)):
+        with pytest.raises(uw.UnweightError) as ei:
+            f()
+        assert ei.value.status == status
