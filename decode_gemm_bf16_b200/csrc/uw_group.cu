@@ -1252,8 +1252,121 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepK = 512;     // k of a CTA: 16 a lane
 constexpr int kPrepRows = 16;   // rows of a CTA: 2 a warp
 
-// Rows of split tiles: CTA (slot tile, 16 of its rows and 512 k); a warp takes
-// two rows, 16 values of each a lane, two lanes a block of 32.  Row r of a tile of n (rounded up
+// 16 values of a row as hi and lo, and the scale byte of their block of 32 (its
+// other half is in the neighbouring lane).
+struct Split16 {
+    uint32_t hi[4], lo[4], sb;
+};
+
+// By fp32, whatever the values: tiny blocks, subnormals, NaN and infinities
+// (which become NaN: e4m3 has no infinity).
+__device__ __noinline__ void split16_any(const uint4 a, const uint4 b, Split16& q) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float v[16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const uint32_t x = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+        if (x < 0x7F800000u) top = top > x ? top : x;
+        else v[i] = __uint_as_float(0x7FC00000u);
+    }
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+    top = top > other ? top : other;
+    // scale 2^s puts the largest into [2^7, 2^8); its byte also has to hold s - 4
+    const uint32_t ex = top >> 23;                        // floor(log2) + 127
+    q.sb = ex > 11u ? ex - 7u : 4u;                       // s + 127
+    const float inv = __uint_as_float((254u - q.sb) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t h2[2];
+        float d[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) d[j] = v[4 * i + j] * inv;
+        asm("{\n\t.reg .b16 x, y;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 x, %4, %3;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 y, %6, %5;\n\t"
+            "mov.b32 %0, {x, y};\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, x;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %2, y;\n\t}"
+            : "=r"(q.hi[i]), "=r"(h2[0]), "=r"(h2[1])
+            : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const __half2 h = *reinterpret_cast<const __half2*>(&h2[j]);
+            d[2 * j] = (d[2 * j] - __low2float(h)) * 16.0f;
+            d[2 * j + 1] = (d[2 * j + 1] - __high2float(h)) * 16.0f;
+        }
+        asm("{\n\t.reg .b16 x, y;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+            "mov.b32 %0, {x, y};\n\t}"
+            : "=r"(q.lo[i])
+            : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+    }
+}
+
+// Blocks whose largest value is a normal number from 2^-104 on (or all zero):
+// in pairs.  x 2^-s as an fp16 number is the BF16 bits with the exponent field
+// moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 of the scaled range
+// (2^-21 of the block's largest) becomes 0.  hi, x - hi and its 16-fold are exact
+// in fp16: they have 8 significant bits at most.
+__device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    uint32_t top = (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+    top = top > other ? top : other;
+    const uint32_t ex = top >> 7;
+    if (__any_sync(0xFFFFFFFFu, (ex < 23u && top) || ex == 255u)) {
+        split16_any(a, b, q);
+        return;
+    }
+    q.sb = top ? ex - 7u : 16u;
+    const uint32_t c = (q.sb - 15u) << 7, c2 = c | (c << 16);
+    const __half2 k16 = __float2half2_rn(16.0f), n16 = __float2half2_rn(-16.0f);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t e[2], r[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const uint32_t x = w[2 * i + j], t = __vmaxu2(x & 0x7FFF7FFFu, c2) - c2;
+            const uint32_t h = (t << 3) | (x & 0x80008000u);
+            e[j] = h;
+        }
+        uint32_t f[2];
+        asm("{\n\t.reg .b16 x, y;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 x, %3;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 y, %4;\n\t"
+            "mov.b32 %0, {x, y};\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, x;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %2, y;\n\t}"
+            : "=r"(q.hi[i]), "=r"(f[0]), "=r"(f[1])
+            : "r"(e[0]), "r"(e[1]));
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const __half2 x = *reinterpret_cast<const __half2*>(&e[j]), h = *reinterpret_cast<const __half2*>(&f[j]);
+            const __half2 d = __hfma2(h, n16, __hmul2(x, k16));
+            r[j] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+        asm("{\n\t.reg .b16 x, y;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+            "mov.b32 %0, {x, y};\n\t}"
+            : "=r"(q.lo[i])
+            : "r"(r[0]), "r"(r[1]));
+    }
+}
+
+// Rows of split tiles: the CTAs of a slot tile share its pieces of 16 rows and
+// 512 k; a warp takes two rows, 16 values of each a lane, two lanes a block of
+// 32.  Row r of a tile of n (rounded up
 // to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
 // swizzled rows; their scale bytes lie in front as tcgen05.cp reads them.
 // Bound by reading the rows and writing as many bytes.
@@ -1277,97 +1390,56 @@ __global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p
     const int64_t s0 = (int64_t)begin[e] + (int64_t)m * each;
     const int nrows = count[e] - m * each < each ? count[e] - m * each : each;
     const int n8 = (nrows + p.round - 1) / p.round * p.round;   // as mma_n
-    const int segs = (int)((p.K + kPrepK - 1) / kPrepK);
-    const int r0 = (int)(blockIdx.y / segs) * kPrepRows + warp;
-    const int64_t k = (int64_t)(blockIdx.y % segs) * kPrepK + 16 * lane;
-    const bool in_k = k < p.K;   // K is a multiple of 128: the 8 lanes of a stage agree
-    uint8_t* out = p.out + ((int64_t)blockIdx.x * p.kt + k / 128) * p.chunk;
-    const int unit = lane & 7;   // 16-byte unit of the stage's row
-    uint4 in[2][2] = {};
-    bool wrong = false;
+    const int segs = (int)((p.K + kPrepK - 1) / kPrepK), items = segs * ((nrows + kPrepRows - 1) / kPrepRows);
+    for (int item = blockIdx.y; item < items; item += gridDim.y) {
+        const int r0 = item / segs * kPrepRows + warp;
+        const int64_t k = (int64_t)(item % segs) * kPrepK + 16 * lane;
+        const bool in_k = k < p.K;   // K is a multiple of 128: the 8 lanes of a stage agree
+        uint8_t* out = p.out + ((int64_t)blockIdx.x * p.kt + k / 128) * p.chunk;
+        const int unit = lane & 7;   // 16-byte unit of the stage's row
+        uint4 in[2][2] = {};
+        bool wrong = false;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int r = r0 + 8 * i;
-        if (r >= nrows) break;
-        int64_t row = s0 + r;
-        if (p.rows) {
-            const int32_t v = p.rows[s0 + r];
-            const bool ok = v >= 0 && v < p.x_rows;
-            wrong |= !ok;
-            row = ok ? v : 0;
-        }
-        if (in_k) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k);
-            in[i][0] = __ldg(src);
-            in[i][1] = __ldg(src + 1);
-        }
-    }
-    if (wrong) raise_status(UW_ERR_DEVICE);
-#pragma unroll
-    for (int i2 = 0; i2 < 2; i2++) {
-        const int r = r0 + 8 * i2;
-        if (r >= nrows) break;
-        const uint4 a = in[i2][0], b = in[i2][1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        float v[16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const uint32_t x = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-            if (x < 0x7F800000u) top = top > x ? top : x;
-            else v[i] = __uint_as_float(0x7FC00000u);   // e4m3 has no infinity: it becomes NaN, as its sums would
-        }
-        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
-        top = top > other ? top : other;
-        // scale 2^s puts the largest into [2^7, 2^8); its byte also has to hold s - 4
-        const uint32_t ex = top >> 23;                        // floor(log2) + 127
-        const uint32_t sb = ex > 11u ? ex - 7u : 4u;          // s + 127
-        const float inv = __uint_as_float((254u - sb) << 23);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            uint32_t h2[2];
-            float d[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) d[j] = v[4 * i + j] * inv;
-            asm("{\n\t.reg .b16 x, y;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f32 x, %4, %3;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f32 y, %6, %5;\n\t"
-                "mov.b32 %0, {x, y};\n\t"
-                "cvt.rn.f16x2.e4m3x2 %1, x;\n\t"
-                "cvt.rn.f16x2.e4m3x2 %2, y;\n\t}"
-                : "=r"(hi[i]), "=r"(h2[0]), "=r"(h2[1])
-                : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const __half2 h = *reinterpret_cast<const __half2*>(&h2[j]);
-                d[2 * j] = (d[2 * j] - __low2float(h)) * 16.0f;
-                d[2 * j + 1] = (d[2 * j + 1] - __high2float(h)) * 16.0f;
+        for (int i = 0; i < 2; i++) {
+            const int r = r0 + 8 * i;
+            if (r >= nrows) break;
+            int64_t row = s0 + r;
+            if (p.rows) {
+                const int32_t v = p.rows[s0 + r];
+                const bool ok = v >= 0 && v < p.x_rows;
+                wrong |= !ok;
+                row = ok ? v : 0;
             }
-            asm("{\n\t.reg .b16 x, y;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
-                "mov.b32 %0, {x, y};\n\t}"
-                : "=r"(lo[i])
-                : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+            if (in_k) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k);
+                in[i][0] = __ldg(src);
+                in[i][1] = __ldg(src + 1);
+            }
         }
-        // the four scale bytes of the stage's row, in every lane of its eight
-        uint32_t sw = sb << (8 * (unit >> 1));
-        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
-        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
-        if (in_k) {
-            const int rh = r, rl = n8 + r;
-            uint8_t* body = out + p.sf_bytes;
-            *reinterpret_cast<uint4*>(body + rh * 128 + ((unit ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(body + rl * 128 + ((unit ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            auto at = [](int row) { return (row >> 7) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4; };
-            if (unit == 0) *reinterpret_cast<uint32_t*>(out + at(rh)) = sw;
-            if (unit == 1) *reinterpret_cast<uint32_t*>(out + at(rl)) = sw - 0x04040404u;
+        if (wrong) raise_status(UW_ERR_DEVICE);
+#pragma unroll
+        for (int i2 = 0; i2 < 2; i2++) {
+            const int r = r0 + 8 * i2;
+            if (r >= nrows) break;
+            const uint4 a = in[i2][0], b = in[i2][1];
+            Split16 q;
+            split16(a, b, q);
+            const uint32_t sb = q.sb;
+            const uint32_t(&hi)[4] = q.hi;
+            const uint32_t(&lo)[4] = q.lo;
+            // the four scale bytes of the stage's row, in every lane of its eight
+            uint32_t sw = sb << (8 * (unit >> 1));
+            sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
+            sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
+            if (in_k) {
+                const int rh = r, rl = n8 + r;
+                uint8_t* body = out + p.sf_bytes;
+                *reinterpret_cast<uint4*>(body + rh * 128 + ((unit ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(body + rl * 128 + ((unit ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                auto at = [](int row) { return (row >> 7) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4; };
+                if (unit == 0) *reinterpret_cast<uint32_t*>(out + at(rh)) = sw;
+                if (unit == 1) *reinterpret_cast<uint32_t*>(out + at(rl)) = sw - 0x04040404u;
+            }
         }
     }
 }
@@ -1623,10 +1695,14 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
         q.sf_bytes = h.sf_b;
         q.chunk = h.chunk;
         q.out = prep;
-        if (src == kGroupMx8)
-            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)((a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows))), 1, kPrepThreads, tab, s, q);
-        else
+        if (src == kGroupMx8) {
+            // about one round of eight CTAs an SM: each lists the tiles once
+            const int64_t pieces = (a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows), round = 8 * (int64_t)P / h.m_tiles;
+            const int64_t y = pieces < round ? pieces : round > 1 ? round : 1;
+            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)y), 1, kPrepThreads, tab, s, q);
+        } else {
             e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), 1, kPrepThreads, 0, s, q);
+        }
         if (e != cudaSuccess) return e;
     }
     const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
