@@ -744,7 +744,12 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // A pair of CTAs works as one on 256 weight rows: each holds its 128 rows
     // and half of the tile's X; the first issues the MMAs of both.
-    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)(blockIdx.x / CG);
+    // Workers count down with the block index: whoever joins a tile's parts
+    // waits for higher workers, that is for blocks that started before it, so
+    // the wait ends even where not all blocks are resident at once, and blocks
+    // that start late, behind the kernel before, are the ones that wait anyway
+    // (300 rows, 4096 x 14336 in BF16: 45 us; counting up, 58).
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)((gridDim.x - 1 - blockIdx.x) / CG);
 
     if (warp == 0) {   // a lane a barrier of each kind
         if (lane < p.S) {
@@ -793,10 +798,11 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         pl.units = pl.ps = pl.parts = pl.rest = 0;
         pl.whole = tiles;
         if (p.parts) {
-            // joining parts takes about 7 us of the first one's time: worth it when that is less than the k steps
-            // (2 cycles a column and step) that the others take off it
+            // joining parts takes about 4.5 us (8600 cycles) of the first one's time: worth it when that is less than the
+            // k steps (2 cycles a column and step) that the others take off it.  (Limits of 3500, 4300 and 7000: 512 rows of
+            // four experts of 2048 x 2048 in BF16 16.2, 14.8, 14.8 us; 256 rows of 14336 x 4096 in 4 bits 32.8, 32.8, 37.5.)
             const uint32_t parts = rest ? P / rest : 0;
-            if (parts > 1 && (uint64_t)p.kt * p.acc_w * (parts - 1) > 7000ull * parts) {
+            if (parts > 1 && (uint64_t)p.kt * p.acc_w * (parts - 1) > 4300ull * parts) {
                 pl.parts = parts;
                 pl.rest = rest;
                 pl.whole = tiles - rest;
@@ -1109,7 +1115,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 }
             };
             if (publish) {
-                float4* dst = reinterpret_cast<float4*>(p.partial) + (size_t)blockIdx.x * slot_f4 + row;
+                float4* dst = reinterpret_cast<float4*>(p.partial) + (size_t)(worker * CG + rank) * slot_f4 + row;
                 for (int c = 0; c < cols; c += 16) {
                     if ((c >> 5 & 1) != set) continue;
                     uint32_t v[16];
@@ -1122,7 +1128,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 }
                 release();   // (synchronises the warp: the tag's release covers every lane's stores)
                 if (lane == 0)
-                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)blockIdx.x * kEpiWarps + warp),
+                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)(worker * CG + rank) * kEpiWarps + warp),
                                  "l"(p.epoch)
                                  : "memory");
             } else {
