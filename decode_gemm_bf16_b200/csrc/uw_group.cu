@@ -1249,14 +1249,14 @@ struct PrepParams {
     const int32_t* offsets;
     int64_t x_rows, slots, K;
     int E, MG, kt, round, step;
+    int steps;                // split rows: 512 k at a time of a warp's item
     uint32_t sf_bytes;        // scale bytes in front of a stage's rows
     int64_t chunk;
     uint8_t* out;
 };
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepK = 512;     // k of a CTA: 16 a lane
-constexpr int kPrepRows = 16;   // rows of a CTA: 2 a warp
+constexpr int kPrepK = 512;     // k of a warp's step: 16 a lane
 
 // 16 values of a row as hi and lo, and the scale byte of their block of 32 (its
 // other half is in the neighbouring lane).
@@ -1316,6 +1316,12 @@ __device__ __noinline__ void split16_any(const uint4 a, const uint4 b, Split16& 
     }
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
 // Blocks whose largest value is a normal number from 2^-104 on (or all zero):
 // in pairs.  x 2^-s as an fp16 number is the BF16 bits with the exponent field
 // moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 of the scaled range
@@ -1325,7 +1331,7 @@ __device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < 8; i++) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
     uint32_t top = (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16;
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
     top = top > other ? top : other;
@@ -1342,7 +1348,7 @@ __device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q
         uint32_t e[2], r[2];
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            const uint32_t x = w[2 * i + j], t = __vmaxu2(x & 0x7FFF7FFFu, c2) - c2;
+            const uint32_t x = w[2 * i + j], t = max_u16x2(x & 0x7FFF7FFFu, c2) - c2;
             const uint32_t h = (t << 3) | (x & 0x80008000u);
             e[j] = h;
         }
@@ -1370,84 +1376,88 @@ __device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q
     }
 }
 
-// Rows of split tiles: the CTAs of a slot tile share its pieces of 16 rows and
-// 512 k; a warp takes two rows, 16 values of each a lane, two lanes a block of
-// 32.  Row r of a tile of n (rounded up
-// to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's 128-byte
-// swizzled rows; their scale bytes lie in front as tcgen05.cp reads them.
-// Bound by reading the rows and writing as many bytes.
-__global__ void __launch_bounds__(kPrepThreads) k_group_split(const PrepParams p) {
+// Rows of split tiles.  A warp takes `steps` (1 or 2) times 512 k of one slot
+// at a time, 16 values a lane and step, two lanes a block of 32; slots are
+// dealt out evenly whatever the groups are.  Row r of a tile of n (rounded up
+// to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's
+// 128-byte swizzled rows; their scale bytes lie in front as tcgen05.cp reads
+// them.
+__global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParams p) {
     extern __shared__ int32_t tab[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int32_t* cum = tab;
     int32_t* begin = cum + p.E + 1;
     int32_t* count = begin + p.E;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     list_tiles(p.offsets, p.E, p.slots, p.MG, 1, cum, begin, count);
-    if ((int)blockIdx.x >= cum[p.E]) return;
-    int e = 0;
-    for (int hi = p.E; hi - e > 1;) {
-        const int mid = (e + hi) >> 1;
-        if (cum[mid] <= (int)blockIdx.x) e = mid; else hi = mid;
-    }
-    const int m = (int)blockIdx.x - cum[e];
-    const int each = tile_slots(count[e], p.MG, p.step);
-    const int64_t s0 = (int64_t)begin[e] + (int64_t)m * each;
-    const int nrows = count[e] - m * each < each ? count[e] - m * each : each;
-    const int n8 = (nrows + p.round - 1) / p.round * p.round;   // as mma_n
-    const int segs = (int)((p.K + kPrepK - 1) / kPrepK), items = segs * ((nrows + kPrepRows - 1) / kPrepRows);
-    for (int item = blockIdx.y; item < items; item += gridDim.y) {
-        const int r0 = item / segs * kPrepRows + warp;
-        const int64_t k = (int64_t)(item % segs) * kPrepK + 16 * lane;
-        const bool in_k = k < p.K;   // K is a multiple of 128: the 8 lanes of a stage agree
-        uint8_t* out = p.out + ((int64_t)blockIdx.x * p.kt + k / 128) * p.chunk;
-        const int unit = lane & 7;   // 16-byte unit of the stage's row
+    if (cum[p.E] == 0) return;
+    uint32_t* each = reinterpret_cast<uint32_t*>(count + p.E);   // slots of an expert's tiles
+    for (int e = threadIdx.x; e < p.E; e += kPrepThreads) each[e] = count[e] ? (uint32_t)tile_slots(count[e], p.MG, p.step) : 1u;
+    __syncthreads();
+    const uint32_t s_first = (uint32_t)begin[0], s_end = (uint32_t)(begin[p.E - 1] + count[p.E - 1]);
+    const uint32_t segs = (uint32_t)((p.K + kPrepK * p.steps - 1) / (kPrepK * p.steps));
+    const uint32_t warps = gridDim.x * (kPrepThreads / 32), ds = warps / segs, dseg = warps % segs;
+    const uint32_t w0 = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+    const int unit = lane & 7;   // 16-byte unit of the stage's row
+    bool wrong = false;
+    uint32_t seg = w0 % segs;
+    for (uint32_t s = s_first + w0 / segs; s < s_end;) {
+        int64_t row = s;
+        if (p.rows) {
+            const int32_t v = __ldg(p.rows + s);
+            const bool ok = v >= 0 && v < p.x_rows;
+            wrong |= !ok;
+            row = ok ? v : 0;
+        }
+        const int k0 = (int)seg * kPrepK * p.steps + 16 * lane;
         uint4 in[2][2] = {};
-        bool wrong = false;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int r = r0 + 8 * i;
-            if (r >= nrows) break;
-            int64_t row = s0 + r;
-            if (p.rows) {
-                const int32_t v = p.rows[s0 + r];
-                const bool ok = v >= 0 && v < p.x_rows;
-                wrong |= !ok;
-                row = ok ? v : 0;
-            }
-            if (in_k) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k);
+        for (int i = 0; i < 2; i++)
+            if (i < p.steps && k0 + i * kPrepK < p.K) {   // K is a multiple of 128: the 8 lanes of a stage agree
+                const uint4* src = reinterpret_cast<const uint4*>(p.X + row * p.K + k0 + i * kPrepK);
                 in[i][0] = __ldg(src);
                 in[i][1] = __ldg(src + 1);
             }
+        // meanwhile: the slot's tile (the last expert that begins at it or before has it)
+        int e = 0;
+        for (int hi = p.E; hi - e > 1;) {
+            const int mid = (e + hi) >> 1;
+            if ((uint32_t)begin[mid] <= s) e = mid; else hi = mid;
         }
-        if (wrong) raise_status(UW_ERR_DEVICE);
+        const uint32_t n = each[e], in_group = s - (uint32_t)begin[e], m = in_group / n;
+        const int rh = (int)(in_group - m * n), left = count[e] - (int)(m * n), nrows = left < (int)n ? left : (int)n;
+        const int rl = ((nrows + p.round - 1) & ~(p.round - 1)) + rh;   // as mma_n
+        uint8_t* tile = p.out + (int64_t)(cum[e] + (int)m) * p.kt * p.chunk;
+        auto at = [](int r) { return (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4; };
+        const int sh = at(rh), sl = at(rl);
+        const uint32_t bh = p.sf_bytes + rh * 128 + ((unit ^ (rh & 7)) << 4), bl = p.sf_bytes + rl * 128 + ((unit ^ (rl & 7)) << 4);
 #pragma unroll
-        for (int i2 = 0; i2 < 2; i2++) {
-            const int r = r0 + 8 * i2;
-            if (r >= nrows) break;
-            const uint4 a = in[i2][0], b = in[i2][1];
+        for (int i = 0; i < 2; i++) {
+            if (i >= p.steps) break;
             Split16 q;
-            split16(a, b, q);
-            const uint32_t sb = q.sb;
-            const uint32_t(&hi)[4] = q.hi;
-            const uint32_t(&lo)[4] = q.lo;
+            split16(in[i][0], in[i][1], q);
             // the four scale bytes of the stage's row, in every lane of its eight
-            uint32_t sw = sb << (8 * (unit >> 1));
+            uint32_t sw = q.sb << (8 * (unit >> 1));
             sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
             sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
-            if (in_k) {
-                const int rh = r, rl = n8 + r;
-                uint8_t* body = out + p.sf_bytes;
-                *reinterpret_cast<uint4*>(body + rh * 128 + ((unit ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(body + rl * 128 + ((unit ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                auto at = [](int row) { return (row >> 7) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4; };
-                if (unit == 0) *reinterpret_cast<uint32_t*>(out + at(rh)) = sw;
-                if (unit == 1) *reinterpret_cast<uint32_t*>(out + at(rl)) = sw - 0x04040404u;
+            const int k = k0 + i * kPrepK;
+            if (k < p.K) {
+                uint8_t* out = tile + (int64_t)(k >> 7) * p.chunk;
+                *reinterpret_cast<uint4*>(out + bh) = make_uint4(q.hi[0], q.hi[1], q.hi[2], q.hi[3]);
+                *reinterpret_cast<uint4*>(out + bl) = make_uint4(q.lo[0], q.lo[1], q.lo[2], q.lo[3]);
+                if (unit == 0) *reinterpret_cast<uint32_t*>(out + sh) = sw;
+                if (unit == 1) *reinterpret_cast<uint32_t*>(out + sl) = sw - 0x04040404u;
             }
         }
+        s += ds;
+        seg += dseg;
+        if (seg >= segs) {
+            seg -= segs;
+            s++;
+        }
     }
+    if (wrong) raise_status(UW_ERR_DEVICE);
 }
 
 // Gathered copy: Xs[s] = X[rows[s]] for the slots of the groups, 16 bytes a
@@ -1702,10 +1712,11 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
         q.chunk = h.chunk;
         q.out = prep;
         if (src == kGroupMx8) {
-            // about one round of eight CTAs an SM: each lists the tiles once
-            const int64_t pieces = (a.K + kPrepK - 1) / kPrepK * ((MG + kPrepRows - 1) / kPrepRows), round = 8 * (int64_t)P / h.m_tiles;
-            const int64_t y = pieces < round ? pieces : round > 1 ? round : 1;
-            e = launch_after(k_group_split, dim3((unsigned)h.m_tiles, (unsigned)y), 1, kPrepThreads, tab, s, q);
+            // warps take two steps at a time where that leaves none idle
+            const int64_t one = a.slots * ((a.K + kPrepK - 1) / kPrepK), most = 4 * (int64_t)P;
+            q.steps = one > 2 * most * (kPrepThreads / 32) ? 2 : 1;
+            const int64_t ctas = (one / q.steps + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+            e = launch_after(k_group_split, dim3((unsigned)(ctas < most ? ctas : most)), 1, kPrepThreads, tab + (size_t)a.E * 4, s, q);
         } else {
             e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), 1, kPrepThreads, 0, s, q);
         }
