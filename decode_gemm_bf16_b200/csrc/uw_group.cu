@@ -1266,7 +1266,9 @@ struct Split16 {
 
 // By fp32, whatever the values: tiny blocks, subnormals, NaN and infinities
 // (which become NaN: e4m3 has no infinity).
-__device__ __noinline__ void split16_any(const uint4 a, const uint4 b, Split16& q) {
+// (By value: a reference would keep every result in local memory.)
+__device__ __noinline__ Split16 split16_any(const uint4 a, const uint4 b) {
+    Split16 q;
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float v[16];
     uint32_t top = 0;
@@ -1314,6 +1316,7 @@ __device__ __noinline__ void split16_any(const uint4 a, const uint4 b, Split16& 
             : "=r"(q.lo[i])
             : "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
     }
+    return q;
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -1323,11 +1326,13 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 
 // Blocks whose largest value is a normal number from 2^-104 on (or all zero):
-// in pairs.  x 2^-s as an fp16 number is the BF16 bits with the exponent field
-// moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 of the scaled range
-// (2^-21 of the block's largest) becomes 0.  hi, x - hi and its 16-fold are exact
-// in fp16: they have 8 significant bits at most.
-__device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q) {
+// in pairs.  |x| 2^-s as an fp16 number v is the BF16 bits with the exponent
+// field moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 of the scaled
+// range (2^-21 of the block's largest) becomes 0.  v 2^-8 has e4m3's exponent
+// field and subnormal range in bits 13..10 and its mantissa below them, so
+// hi is its upper bits, cut off; the rest, at most 4 significant bits
+// where hi is normal, gives lo the same way, rounded.
+__device__ __forceinline__ Split16 split16(const uint4 a, const uint4 b) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t m = 0;
 #pragma unroll
@@ -1336,44 +1341,28 @@ __device__ __forceinline__ void split16(const uint4 a, const uint4 b, Split16& q
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
     top = top > other ? top : other;
     const uint32_t ex = top >> 7;
-    if (__any_sync(0xFFFFFFFFu, (ex < 23u && top) || ex == 255u)) {
-        split16_any(a, b, q);
-        return;
-    }
+    if (__any_sync(0xFFFFFFFFu, (ex < 23u && top) || ex == 255u)) return split16_any(a, b);
+    Split16 q;
     q.sb = top ? ex - 7u : 16u;
     const uint32_t c = (q.sb - 15u) << 7, c2 = c | (c << 16);
-    const __half2 k16 = __float2half2_rn(16.0f), n16 = __float2half2_rn(-16.0f);
+    const __half2 down8 = __float2half2_rn(0x1p-8f), down4 = __float2half2_rn(0x1p-4f), n16 = __float2half2_rn(-16.0f);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        uint32_t e[2], r[2];
+        uint32_t hi[2], lo[2];
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            const uint32_t x = w[2 * i + j], t = max_u16x2(x & 0x7FFF7FFFu, c2) - c2;
-            const uint32_t h = (t << 3) | (x & 0x80008000u);
-            e[j] = h;
+            const uint32_t t = (max_u16x2(w[2 * i + j] & 0x7FFF7FFFu, c2) - c2) << 3;
+            const __half2 v = *reinterpret_cast<const __half2*>(&t), u = __hmul2(v, down8);
+            const uint32_t ub = *reinterpret_cast<const uint32_t*>(&u), hb = ub & 0xFF80FF80u;
+            const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&hb), n16, __hmul2(v, down4));   // 16 (v 2^-8 - hi 2^-8)
+            hi[j] = ub << 1;
+            lo[j] = (*reinterpret_cast<const uint32_t*>(&r) << 1) + 0x00800080u;
         }
-        uint32_t f[2];
-        asm("{\n\t.reg .b16 x, y;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 x, %3;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 y, %4;\n\t"
-            "mov.b32 %0, {x, y};\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, x;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %2, y;\n\t}"
-            : "=r"(q.hi[i]), "=r"(f[0]), "=r"(f[1])
-            : "r"(e[0]), "r"(e[1]));
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const __half2 x = *reinterpret_cast<const __half2*>(&e[j]), h = *reinterpret_cast<const __half2*>(&f[j]);
-            const __half2 d = __hfma2(h, n16, __hmul2(x, k16));
-            r[j] = *reinterpret_cast<const uint32_t*>(&d);
-        }
-        asm("{\n\t.reg .b16 x, y;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
-            "mov.b32 %0, {x, y};\n\t}"
-            : "=r"(q.lo[i])
-            : "r"(r[0]), "r"(r[1]));
+        const uint32_t sign = prmt(w[2 * i], w[2 * i + 1], 0x7531u) & 0x80808080u;
+        q.hi[i] = prmt(hi[0], hi[1], 0x7531u) | sign;
+        q.lo[i] = prmt(lo[0], lo[1], 0x7531u) | sign;
     }
+    return q;
 }
 
 // Rows of split tiles.  A warp takes `steps` (1 or 2) times 512 k of one slot
@@ -1435,8 +1424,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParam
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             if (i >= p.steps) break;
-            Split16 q;
-            split16(in[i][0], in[i][1], q);
+            const Split16 q = split16(in[i][0], in[i][1]);
             // the four scale bytes of the stage's row, in every lane of its eight
             uint32_t sw = q.sb << (8 * (unit >> 1));
             sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
