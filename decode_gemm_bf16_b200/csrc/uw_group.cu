@@ -21,7 +21,7 @@
 //     cut tile's first k steps adds the others' fp32 partial sums in k order
 //     (from the workspace; deterministic);
 //   * warp roles: 0-7 epilogue, 8 and 11 TMA producers of weights and of X, 9 MMA
-//     issue (10: see kMix; 12-19: see kGroupMx);
+//     issue (10 and 12: see kMix; 12-19: see kGroupMx);
 //   * 4-bit weights with BF16 rows (kGroupMx8): the tensor cores take the codes
 //     and scales as they are, against 8-bit rows.  A BF16 value has 8
 //     significant bits, an e4m3 value 4: x = 2^s (hi + lo/16) with both in
@@ -40,13 +40,28 @@
 //     format stores them;
 //   * gathered BF16 rows: tiles of up to 32 slots take them by TMA (four row
 //     indices a request), larger ones from a gathered copy (k_group_gather):
-//     a request of four rows of 128 bytes takes about 34 cycles, a row of a
-//     box about 2;
+//     a request of four rows of 128 bytes takes about 34 cycles, so 256 rows a
+//     stage would take four times as long as the stage's MMAs;
 //   * after one of these two kernels the weights of the first stages are
 //     requested before the wait on it: it lets this kernel start only after
 //     its own wait, so everything it does not write is complete;
 //   * every wait is bounded; on expiry the CTA raises UW_ERR_TIMEOUT, drains
 //     its own copies and MMAs, frees tensor memory and returns.
+//
+// Measured (one B200, GPU time alone, copy bandwidth 6.5 TB/s, library BF16
+// product 1.63 PFLOP/s for a burst, 1.39 held):
+//   BF16, gate and up of 8 experts of 14336 x 4096, 16 slots: 278 us, 6.8 TB/s
+//     of weights;
+//   BF16, 8 experts of 800-1493 rows, 4096 x 14336: 740 us, 1.30 PFLOP/s (1.11
+//     held: the power limit), tensor pipe 96 % active; one group of 8192 rows
+//     630 us, 1.53 (1.30 held, where the library's product has 1.31);
+//   4-bit weights, 128 experts of 768 x 2048 twice, 264 slots: 49 us, 3.9 TB/s
+//     of weights; 8 experts of 14336 x 4096 twice, 16 slots: 96 us, 5.2 TB/s;
+//   4-bit weights, 64 experts of 1408 x 2048 twice, 12288 slots: 149 us, 0.95
+//     PFLOP/s (22 us of it the split rows); 4480 rows of 8192 x 4096: 204 us,
+//     1.47 PFLOP/s;
+//   both in 4 bits, 2048 rows of 14336 x 4096: 51 us, 4.7 PFLOP/s; 8192^3: 192
+//     us, 5.7 PFLOP/s.
 #include <cuda_fp16.h>
 
 #include "uw_device.cuh"
@@ -61,9 +76,9 @@ namespace {
 constexpr int kTileN = 128;            // weight rows of a tile
 constexpr int kProd = 8, kMma = 9, kRebuild0 = 12, kRebuildWarps = 8;
 constexpr int kEpiWarps = 8;           // two per quarter of tensor memory's lanes
-constexpr int kMix = 10;               // kGroupMx8: warp that joins the scales of two weights
+constexpr int kMix = 10, kMix2 = 12;    // kGroupMx8: warps that join the scales of two weights, every other stage each
 constexpr int kRows = 11;              // TMA producer of X
-constexpr int kThreadsPlain = 12 * 32;
+constexpr int kThreadsPlain = 12 * 32, kThreadsMix = 13 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
 constexpr int kMaxS = 12;              // stages
 constexpr int kMaxT = 8;               // rebuilt-A slots in tensor memory
@@ -994,19 +1009,23 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         mbar_wait(fin, 0, p.timeout, nullptr);
         }
         __syncwarp();
-    } else if (SRC == kGroupMx8 && warp == kMix) {
+    } else if (SRC == kGroupMx8 && (warp == kMix || warp == kMix2)) {
         // ------------------------------------------------------------ scales of two weights
         // The tile's 128 rows are 64 of W and 64 of `up`, halves of a 128-row
         // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
-        // either into the 16 bytes that tensor memory takes for lane l.
+        // either into the 16 bytes that tensor memory takes for lane l.  A stage
+        // costs a warp some 450 cycles of latency, so two take turns (8 experts of
+        // 14336 x 4096 twice, 16 rows: 96 us, 108 with one).
         if (p.up) {
+            int turn = warp == kMix ? 0 : 1;
             Walk wk(work, worker);
             Seg sg;
             Ring r;
             bool ok = true;
             Tile t;
             while (ok && wk.next(p, pl, sg, t)) {
-                for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
+                for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S), turn ^= 1) {
+                    if (turn) continue;
                     if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
                     const uint32_t at = ss + (uint32_t)(lane * 16 + ((t.n * CG + rank) & 1) * 8);
@@ -1232,7 +1251,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 }
 
 template <int SRC, int CG>
-__global__ void __launch_bounds__(kThreadsPlain, 1)
+__global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
     k_group(const __grid_constant__ Maps m, const GroupParams p) {
     group_body<SRC, CG>(m, p);
 }
@@ -1370,7 +1389,9 @@ __device__ __forceinline__ Split16 split16(const uint4 a, const uint4 b) {
 // dealt out evenly whatever the groups are.  Row r of a tile of n (rounded up
 // to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's
 // 128-byte swizzled rows; their scale bytes lie in front as tcgen05.cp reads
-// them.
+// them.  Reads and writes stay in L2 mostly (a row is read once for each of its
+// slots); bound by instructions, about 11 a value pair (12288 slots of 2048: 22
+// us, 2.3 TB/s each way; 4480 rows of 4096: 16 us).
 __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParams p) {
     extern __shared__ int32_t tab[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1449,7 +1470,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParam
 }
 
 // Gathered copy: Xs[s] = X[rows[s]] for the slots of the groups, 16 bytes a
-// thread and step.
+// thread and step, four in flight.  Bound by reading and writing a row a slot.
 __global__ void __launch_bounds__(kPrepThreads) k_group_gather(const PrepParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1712,7 +1733,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     }
     const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
     return launch_after(kern, dim3((unsigned)(workers * CG)), CG,
-                        src == kGroupMx ? kThreadsRebuild : kThreadsPlain, smem, s, m, p);
+                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 && p.up ? kThreadsMix : kThreadsPlain, smem, s, m, p);
 }
 
 }  // namespace uw

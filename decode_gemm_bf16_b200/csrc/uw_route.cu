@@ -16,12 +16,16 @@
 // warps before each warp.  Ranks inside a warp come from match_any, so the
 // order -- and every output -- is the same on every run.  What bounds it: the
 // logits are read once; below a few thousand tokens the launches' latency.
-// With few choices one CTA does both parts in a single launch.
+// With few choices one CTA does both parts in a single launch.  Measured: 16
+// tokens of 64 experts, k = 6: 5.3 us; 16384 tokens of 256 experts in fp32, k = 8:
+// 24 us against 2.9 us for the bytes, two thirds of it the rounds (32 keys a
+// lane, 9 rounds), the rest counting and placing.
 //
 // Combination.  Y[t] = sum_j w[t,j] Z[pos[t,j]]: bound by reading T k N and
 // writing T N values once.  A warp owns 256 columns of one token at a time, 8 a
 // lane; lane j holds choice j, and the next item's choices are loaded before
-// the eight rows in flight are added.
+// the eight rows in flight are added.  Measured: 8192 tokens of 8 rows of 4096 in
+// BF16: 100 us, 6.1 TB/s; 8 tokens of 2 rows: 2.5 us.
 #include "uw_device.cuh"
 #include "uw_internal.h"
 
