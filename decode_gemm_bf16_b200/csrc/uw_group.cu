@@ -26,8 +26,8 @@
 //     and scales as they are, against 8-bit rows.  A BF16 value has 8
 //     significant bits, an e4m3 value 4: x = 2^s (hi + lo/16) with both in
 //     e4m3 and 2^s the scale of its block of 32 is exact for every x of at
-//     least 2^-13 times the block's largest, and off by at most 2^-21 of that
-//     largest below.  hi and lo are two rows of the MMA's N, added in fp32 at
+//     least 2^-13 times the block's largest, and off by at most 2^-21 (1 + 2^-8)
+//     of that largest below.  hi and lo are two rows of the MMA's N, added in fp32 at
 //     the end: the operations of a BF16 product at twice the rate, and no
 //     rebuilt weights.  A first kernel (k_group_split) writes the rows of
 //     every tile in the order of its stages' shared memory, gathered, split
@@ -1346,8 +1346,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 // Blocks whose largest value is a normal number from 2^-104 on (or all zero):
 // in pairs.  |x| 2^-s as an fp16 number v is the BF16 bits with the exponent
-// field moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 of the scaled
-// range (2^-21 of the block's largest) becomes 0.  v 2^-8 has e4m3's exponent
+// field moved, (bits - ((s + 112) << 7)) << 3; what is below 2^-14 there (2^-21 of
+// the block's largest) lands somewhere below 2^-14.  v 2^-8 has e4m3's exponent
 // field and subnormal range in bits 13..10 and its mantissa below them, so
 // hi is its upper bits, cut off; the rest, at most 4 significant bits
 // where hi is normal, gives lo the same way, rounded.
@@ -1390,8 +1390,8 @@ __device__ __forceinline__ Split16 split16(const uint4 a, const uint4 b) {
 // to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's
 // 128-byte swizzled rows; their scale bytes lie in front as tcgen05.cp reads
 // them.  Reads and writes stay in L2 mostly (a row is read once for each of its
-// slots); bound by instructions, about 11 a value pair (12288 slots of 2048: 22
-// us, 2.3 TB/s each way; 4480 rows of 4096: 16 us).
+// slots); bound by instructions (12288 slots of 2048: 22 us, 2.3 TB/s each way;
+// 4480 rows of 4096: 16 us).
 __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParams p) {
     extern __shared__ int32_t tab[];
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -14,8 +14,8 @@
 // tile's 1024 scale bytes are gathered in shared memory and leave as one
 // contiguous run.  The CTA's rows are loaded eight steps ahead of their use.
 // Measured: 14336 x 4096 from fp32 and back to BF16 in 77 us for both, 5.4 TB/s
-// (the copy bandwidth is 6.5); 2048 x 4096 from BF16 in 11 us, of which the
-// launch and one tile's latency are half.
+// (the copy bandwidth is 6.5); 37 x 4096 from BF16 and back in 4.6 us, two
+// launches' latency.
 #include <cuda_fp16.h>
 
 #include "uw_device.cuh"

@@ -414,8 +414,8 @@ uw_status uw_mx_dequantize(const uw_mx_matrix* m, void* out, int out_f32, void* 
  *   X: device BF16 [M,K].  With K a multiple of 128 each value enters the
  *     8-bit tensor cores as 2^s (hi + lo/16), 2^s the scale of its block of 32
  *     along K: exactly, if it is at least 2^-13 times the block's largest;
- *     below, off by at most 2^-21 of that largest (2^-137 in a block whose
- *     largest is below 2^-115).
+ *     below, off by at most 2^-21 (1 + 2^-8) of that largest (2^-137 in a
+ *     block whose largest is below 2^-115).
  *     An infinity in X counts as NaN.  With other K the weights are rebuilt to
  *     BF16 on chip, exactly wherever BF16 holds the value.
  *   X_mx: MXFP4 [M,K] (batch 1; M = its rows): block-scaled 4-bit products.

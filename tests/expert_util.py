@@ -88,9 +88,12 @@ def product_tolerance(absolute: torch.Tensor, K: int) -> torch.Tensor:
 
 
 def split_tolerance(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
-    """BF16 rows against 4-bit weights: a value may enter the product off by 2^-21 of the largest of its block of 32."""
+    """BF16 rows against 4-bit weights: a value may enter the product off by 2^-21 (1 + 2^-8) of the largest of its
+    block of 32.  The largest is scaled into [2^7, 2^8) and lo has steps of 2^-13 there, so rounding is off by 2^-14 at
+    most; below 2^-14 a value with significand 1 + m/128 is taken as m/128 2^-14, which for m = 127, whose tie goes up to
+    2^-13, is (2 - 255/256) 2^-14."""
     top = X.abs().unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1)
-    return 2.0 ** -21 * (top @ W.abs().T)
+    return 2.0 ** -21 * (1 + 2.0 ** -8) * (top @ W.abs().T)
 
 
 def swiglu_ref(g: torch.Tensor, u: torch.Tensor) -> torch.Tensor:
