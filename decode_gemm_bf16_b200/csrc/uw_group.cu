@@ -822,7 +822,13 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 pl.rest = rest;
                 pl.whole = tiles - rest;
             }
-        } else if (rest) {
+        } else if (rest && (uint64_t)p.kt * (P - rest) > (uint64_t)(rounds ? 10 : 24) * P) {
+            // Ranges take kt (P - rest) / P steps off the longest worker and cost it a joining: worth it from 10 steps on,
+            // 24 where no whole round comes first (then all memory bandwidth is close to used without them).  Whole tiles
+            // against ranges, 64 rows in BF16: 12800 x 4096 (21 steps) 24.1 and 26.9 us, 16384 x 8192 (17) 49.0 and 52.6,
+            // 9600 x 4096 (32) 21.5 and 22.7; one row in 4 bits: 14336 x 4096 (8) 13.8 and 14.8, 7000 x 4096 (20) 12.9
+            // and 12.3, 9600 x 8192 (32) 18.9 and 16.7; behind a whole round: 18000 x 4096 (2) 14.1 and 15.5, 30000 x 4096
+            // (13) 20.3 and 19.4.
             pl.whole = rounds > 1 ? (rounds - 1) * P : 0;
             pl.units = (tiles - pl.whole) * (uint32_t)p.kt;
             // a range shorter than two k steps costs more to join than it saves

@@ -535,6 +535,19 @@ def test_grouped_rounds_and_cut_tiles(mx, up, R):
         U.check(uw.uw_gemm_grouped(X, W[0], off, up=W[1] if up else None), ref, tol)
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [([1, 0, 17, 5], 520, 8192), ([1, 0, 17, 5], 520, 8256), ([4] * 8, 2600, 4096),
+                                       ([4] * 8, 2600, 4160)])
+def test_grouped_small_tiles_cut_in_ranges(mx, up, sizes, N, K):
+    """A long K with few tiles, or a few behind a whole round: workers share tiles of few slots; the same bits every time."""
+    X, W, off, rows, ref, tol = _grouped_case(sizes, N, K, mx, up, True)
+    y = uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1] if up else None)
+    U.check(y, ref, tol)
+    for _ in range(3):
+        assert torch.equal(y, uw.uw_gemm_grouped(X, W[0], off, rows=rows, up=W[1] if up else None))
+
+
 def test_grouped_outputs_past_32_bits():
     """2.3e9 outputs: the last slots' addresses pass 2^31 elements and 2^32 bytes."""
     R, N, K = 70000, 32768, 64
