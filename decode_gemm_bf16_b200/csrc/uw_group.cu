@@ -17,7 +17,7 @@
 //     at the same time share weight tiles and slot tiles in L2;
 //   * one persistent CTA per SM, in pairs (cta_group::2: one MMA over 256 weight
 //     rows) where tiles are large.  Full rounds of whole tiles are dealt out one
-//     a worker; what is left over is cut along k (see Plan).  The worker with a
+//     a worker; what is left over is cut along k where that pays (see Plan).  The worker with a
 //     cut tile's first k steps adds the others' fp32 partial sums in k order
 //     (from the workspace; deterministic);
 //   * warp roles: 0-7 epilogue, 8 and 11 TMA producers of weights and of X, 9 MMA
