@@ -12,6 +12,7 @@ LIB = os.path.join(HERE, "libunweight.so")
 SOURCES = ["uw_host.cpp", "uw_compress.cu", "uw_decode.cu", "uw_gemm.cu", "uw_gemv.cu", "uw_mx.cu",
            "uw_route.cu", "uw_group.cu", "uw_experts.cpp"]
 HEADERS = ["uw_internal.h", "uw_device.cuh", os.path.join("..", "..", "include", "unweight.h")]
+UNIT_HEADERS = {"uw_group.cu": ["uw_plan.h"]}   # of one unit alone
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 BUILD_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler",
                "-fvisibility=default", "--expt-relaxed-constexpr"]
@@ -27,7 +28,8 @@ STAMP = LIB + ".srchash"
 
 def source_hash() -> str:
     h = hashlib.sha256()
-    for f in SOURCES + HEADERS + [os.path.abspath(__file__)]:
+    own = [f for fs in UNIT_HEADERS.values() for f in fs]
+    for f in SOURCES + HEADERS + own + [os.path.abspath(__file__)]:
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()
@@ -65,7 +67,8 @@ def code_hash(unit: str | None = None) -> str:
     headers count, so a measurement of its kernels survives changes to the
     other units."""
     h = hashlib.sha256(" ".join(ARCH + BUILD_FLAGS).encode())
-    for f in ([unit] if unit else SOURCES) + HEADERS:
+    units = [unit] if unit else SOURCES
+    for f in units + HEADERS + [f for u in units for f in UNIT_HEADERS.get(u, [])]:
         with open(os.path.join(CSRC, f), encoding="utf-8") as fh:
             h.update(_strip_comments(fh.read()).encode())
     return h.hexdigest()

@@ -17,7 +17,7 @@
 //     at the same time share weight tiles and slot tiles in L2;
 //   * one persistent CTA per SM, in pairs (cta_group::2: one MMA over 256 weight
 //     rows) where tiles are large.  Full rounds of whole tiles are dealt out one
-//     a worker; what is left over is cut along k where that pays (see Plan).  The worker with a
+//     a worker; what is left over is cut along k where that pays (uw_plan.h).  The worker with a
 //     cut tile's first k steps adds the others' fp32 partial sums in k order
 //     (from the workspace; deterministic);
 //   * warp roles: 0-7 epilogue, 8 and 11 TMA producers of weights and of X, 9 MMA
@@ -66,6 +66,7 @@
 
 #include "uw_device.cuh"
 #include "uw_internal.h"
+#include "uw_plan.h"
 
 namespace uw {
 
@@ -108,7 +109,7 @@ struct GroupParams {
     uint32_t sf_slot;                       // scale columns of a stage
     uint32_t a_col0, sf_col0;
     int step;                               // tiles of a group hold a multiple of this many slots
-    int parts;                              // cut tiles in equal parts (see Plan)
+    int parts;                              // cut tiles in equal parts (uw_plan.h)
     int early;                              // a preparing kernel of this call ran just before
     const uint8_t* prep;                    // kGroupMx8: [slot tiles][kt][scales, rows]
     int64_t prep_chunk;                     // bytes of one stage of one tile there
@@ -137,26 +138,11 @@ struct Ring {
     }
 };
 
-// The tile list as every role sees it (shared memory) and how it is shared
-// out.  Whole tiles are dealt out in rounds, one a worker (a CTA or a pair).
-// The rest is cut along k, either
-//   * in equal contiguous ranges of k steps, one a worker (`ps` workers), or
-//   * (parts > 0) every one of the last `rest` tiles in `parts` equal parts,
-//     worker part * rest + i taking a part of tile i.
-struct Plan {
+// The tile list as every role sees it (shared memory).
+struct Tiles {
     const int32_t* cum;      // [E + 1] tiles before each expert
     const int32_t* begin;    // [E] first slot
     const int32_t* count;    // [E] slots
-    uint32_t whole;          // tiles dealt out whole (the first ones)
-    uint32_t units;          // k steps of the cut tiles (contiguous ranges; the host checks that units * P < 2^32)
-    uint32_t ps;             // of the P workers, those that share them
-    uint32_t P;
-    uint32_t parts, rest;
-};
-
-struct Seg {
-    uint32_t tile;
-    int kt0, kt1;
 };
 
 // Slots of a tile of a group of c: the group is cut into as few tiles of at
@@ -176,40 +162,6 @@ struct Tile {
     int64_t m;               // the slot tile's number among all
 };
 
-// Units of worker b's range start here; owner of a unit.
-__device__ __forceinline__ uint32_t unit_begin(uint32_t b, const Plan& pl) { return b * pl.units / pl.ps; }
-__device__ __forceinline__ uint32_t unit_owner(uint32_t u, const Plan& pl) { return ((u + 1) * pl.ps - 1) / pl.units; }
-
-// Segment i of worker b: its range or part of the cut tiles first (joining them
-// then overlaps the whole tiles), then its whole tiles.
-__device__ __forceinline__ bool segment(const Plan& pl, uint32_t b, uint32_t i, uint32_t kt, Seg& s) {
-    if (b < pl.ps) {
-        const uint32_t u0 = unit_begin(b, pl), ue = unit_begin(b + 1, pl), t0 = u0 / kt;
-        const uint32_t n = ue > u0 ? (ue - 1) / kt - t0 + 1 : 0;
-        if (i < n) {
-            const uint32_t tile0 = (t0 + i) * kt, end = tile0 + kt < ue ? tile0 + kt : ue;
-            s.tile = pl.whole + t0 + i;
-            s.kt0 = i ? 0 : (int)(u0 - tile0);
-            s.kt1 = (int)(end - tile0);
-            return true;
-        }
-        i -= n;
-    } else if (b < pl.parts * pl.rest) {
-        if (i == 0) {
-            const uint32_t part = b / pl.rest;
-            s.tile = pl.whole + b - part * pl.rest;
-            s.kt0 = (int)(part * kt / pl.parts);
-            s.kt1 = (int)((part + 1) * kt / pl.parts);
-            return true;
-        }
-        i--;
-    }
-    s.tile = b + i * pl.P;
-    s.kt0 = 0;
-    s.kt1 = (int)kt;
-    return s.tile < pl.whole;
-}
-
 // A worker's segments with their tiles.  The first kListed are worked out by
 // the block's threads at once when it starts (in every role, one after the
 // other, they cost 1700 cycles a tile).
@@ -219,16 +171,16 @@ struct Work {
     Tile tile;
 };
 
-__device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, uint32_t utile) {
+__device__ __forceinline__ Tile locate(const GroupParams& p, const Tiles& tl, uint32_t utile) {
     const int tile = (int)utile;   // below 2^31
     int lo = 0, hi = p.E;   // last expert with cum[e] <= tile (experts without tiles are passed over)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (pl.cum[mid] <= tile) lo = mid; else hi = mid;
+        if (tl.cum[mid] <= tile) lo = mid; else hi = mid;
     }
-    const int c = pl.count[lo];
+    const int c = tl.count[lo];
     const int mt = (c + p.MG - 1) / p.MG;
-    int l = tile - pl.cum[lo];
+    int l = tile - tl.cum[lo];
     const int band = l / (kBand * p.n_tiles);
     l -= band * kBand * p.n_tiles;
     const int nb = mt - band * kBand < kBand ? mt - band * kBand : kBand;
@@ -237,8 +189,8 @@ __device__ __forceinline__ Tile locate(const GroupParams& p, const Plan& pl, uin
     t.n = l / nb;
     const int m = band * kBand + l % nb;
     const int each = tile_slots(c, p.MG, p.step);
-    t.s0 = (int64_t)pl.begin[lo] + (int64_t)m * each;
-    t.m = pl.cum[lo] / p.n_tiles + m;
+    t.s0 = (int64_t)tl.begin[lo] + (int64_t)m * each;
+    t.m = tl.cum[lo] / p.n_tiles + m;
     t.rows = c - m * each < each ? c - m * each : each;
     return t;
 }
@@ -247,16 +199,16 @@ struct Walk {
     const Work* list;
     int worker, i = 0;
     __device__ __forceinline__ Walk(const Work* l, int b) : list(l), worker(b) {}
-    __device__ __forceinline__ bool next(const GroupParams& p, const Plan& pl, Seg& s, Tile& t) {
+    __device__ __forceinline__ bool next(const GroupParams& p, const Tiles& tl, const Plan& pl, Seg& s, Tile& t) {
         if (i < kListed) {
             s = list[i].seg;
             t = list[i].tile;
             i++;
             return t.rows > 0;
         }
-        if (!segment(pl, (uint32_t)worker, (uint32_t)i, (uint32_t)p.kt, s)) return false;
+        if (!segment(pl, (uint32_t)worker, (uint32_t)i, s)) return false;
         i++;
-        t = locate(p, pl, s.tile);
+        t = locate(p, tl, s.tile);
         return true;
     }
 };
@@ -803,43 +755,12 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Plan pl;
-    pl.cum = cum;
-    pl.begin = begin;
-    pl.count = count;
-    {
-        const uint32_t tiles = (uint32_t)cum[p.E], P = gridDim.x / CG, rounds = tiles / P, rest = tiles - rounds * P;
-        pl.P = P;
-        pl.units = pl.ps = pl.parts = pl.rest = 0;
-        pl.whole = tiles;
-        if (p.parts) {
-            // joining parts takes about 4.5 us (8600 cycles) of the first one's time: worth it when that is less than the
-            // k steps (2 cycles a column and step) that the others take off it.  (Limits of 3500, 4300 and 7000: 512 rows of
-            // four experts of 2048 x 2048 in BF16 16.2, 14.8, 14.8 us; 256 rows of 14336 x 4096 in 4 bits 32.8, 32.8, 37.5.)
-            const uint32_t parts = rest ? P / rest : 0;
-            if (parts > 1 && (uint64_t)p.kt * p.acc_w * (parts - 1) > 4300ull * parts) {
-                pl.parts = parts;
-                pl.rest = rest;
-                pl.whole = tiles - rest;
-            }
-        } else if (rest && (uint64_t)p.kt * (P - rest) > (uint64_t)(rounds ? 10 : 24) * P) {
-            // Ranges take kt (P - rest) / P steps off the longest worker and cost it a joining: worth it from 10 steps on,
-            // 24 where no whole round comes first (then all memory bandwidth is close to used without them).  Whole tiles
-            // against ranges, 64 rows in BF16: 12800 x 4096 (21 steps) 24.1 and 26.9 us, 16384 x 8192 (17) 49.0 and 52.6,
-            // 9600 x 4096 (32) 21.5 and 22.7; one row in 4 bits: 14336 x 4096 (8) 13.8 and 14.8, 7000 x 4096 (20) 12.9
-            // and 12.3, 9600 x 8192 (32) 18.9 and 16.7; behind a whole round: 18000 x 4096 (2) 14.1 and 15.5, 30000 x 4096
-            // (13) 20.3 and 19.4.
-            pl.whole = rounds > 1 ? (rounds - 1) * P : 0;
-            pl.units = (tiles - pl.whole) * (uint32_t)p.kt;
-            // a range shorter than two k steps costs more to join than it saves
-            const uint32_t most = (pl.units + 1) / 2;
-            pl.ps = P < most ? P : most;
-        }
-    }
+    const Tiles tl{cum, begin, count};
+    const Plan pl = make_plan((uint32_t)cum[p.E], gridDim.x / CG, (uint32_t)p.kt, p.acc_w, p.parts != 0);
     Work* work = reinterpret_cast<Work*>(smem + p.work_off);
     for (int i = threadIdx.x; i < kListed; i += blockDim.x) {
         Work w;
-        if (segment(pl, (uint32_t)worker, (uint32_t)i, (uint32_t)p.kt, w.seg)) w.tile = locate(p, pl, w.seg.tile);
+        if (segment(pl, (uint32_t)worker, (uint32_t)i, w.seg)) w.tile = locate(p, tl, w.seg.tile);
         else w.tile.rows = 0;
         work[i] = w;
     }
@@ -862,7 +783,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             const uint32_t sig = CG == 2 ? in_first(full) - full : 0;   // from a barrier here to the first CTA's
             bool ok = true;
             Tile t;
-            while (ok && wk.next(p, pl, sg, t)) {
+            while (ok && wk.next(p, tl, pl, sg, t)) {
                 Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
@@ -892,7 +813,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             const uint32_t sig = CG == 2 ? in_first(full) - full : 0;
             bool ok = true;
             Tile t;
-            while (ok && wk.next(p, pl, sg, t)) {
+            while (ok && wk.next(p, tl, pl, sg, t)) {
                 Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
                 int4 idx[8];
                 if (CG == 1 && p.rows) {
@@ -938,7 +859,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         uint32_t ph = 0, fb = full, lo = lo0, sf = tmem + p.sf_col0;
         bool ok = true;
         Tile t;
-        while (ok && wk.next(p, pl, sg, t)) {
+        while (ok && wk.next(p, tl, pl, sg, t)) {
             const int nN = mma_n<SRC, CG>(t.rows);
             const uint32_t idesc = SRC == kGroupMx8    ? idesc_mx8(CG, nN, 0)
                                    : SRC == kGroupMxMx ? idesc_mx(CG, nN, 0)
@@ -1029,7 +950,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             Ring r;
             bool ok = true;
             Tile t;
-            while (ok && wk.next(p, pl, sg, t)) {
+            while (ok && wk.next(p, tl, pl, sg, t)) {
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S), turn ^= 1) {
                     if (turn) continue;
                     if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
@@ -1061,7 +982,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         Ring r, rt;
         bool ok = true;
         Tile t;
-        while (ok && wk.next(p, pl, sg, t)) {
+        while (ok && wk.next(p, tl, pl, sg, t)) {
             // where this row's scale bytes are in the stage
             uint32_t so = p.off_s;
             int sq = quarter;
@@ -1100,14 +1021,12 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         Seg sg;
         Ring ra;
         Tile t;
-        while (wk.next(p, pl, sg, t)) {
+        while (wk.next(p, tl, pl, sg, t)) {
             const int cols = (t.rows + 15) & ~15;
             const uint32_t lo = (uint32_t)(mma_n<SRC, CG>(t.rows) / 2);   // split rows: first lo column
-            const bool publish = sg.kt0 > 0, joins = sg.kt0 == 0 && sg.kt1 < p.kt;
+            const bool publish = publishes(sg);
             // the tile's other ranges, in k order: workers worker + stride, ... up to `last`
-            const int stride = pl.parts ? (int)pl.rest : 1;
-            int last = worker;
-            if (joins) last = pl.parts ? worker + (int)(pl.parts - 1) * stride : (int)unit_owner((sg.tile - pl.whole + 1) * (uint32_t)p.kt - 1, pl);
+            const int stride = (int)join_stride(pl), last = (int)last_joined(pl, sg, (uint32_t)worker);
             bool good = true;
             for (int b = worker + stride; good && b <= last; b += stride)
                 good = wait_tag(p.flags + (size_t)(b * CG + rank) * kEpiWarps + warp, p.epoch, p.timeout, abort_flag);

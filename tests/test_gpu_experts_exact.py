@@ -1,0 +1,97 @@
+"""Grouped and 4-bit products on whole numbers: every sum is exact in fp32 in any
+order, so one product left out, taken twice or scaled wrongly shows, and so does
+an output that was not written."""
+import numpy as np
+import pytest
+import torch
+
+import decode_gemm_bf16_b200 as uw
+from tests import expert_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    assert uw.uw_last_device_status() == 0
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _rows(M, K, seed, step=1.0):
+    """Whole numbers from -3 to 3, times a power of two: exact in BF16, in two 8-bit halves and in 4 bits."""
+    return (torch.randint(-3, 4, (M, K), generator=_gen(seed), device="cuda") * step).to(torch.bfloat16)
+
+
+def _weights(E, N, K, seed):
+    """Whole numbers from -3 to 3, every block of 32 times 1, 2 or 4: exact in BF16 and in 4 bits; below 2^24 in sums of K < 2^17."""
+    w = torch.randint(-3, 4, (E, N, K), generator=_gen(seed), device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    s = torch.randint(0, 3, (E, N, K // 32), generator=_gen(seed + 1), device="cuda").to(torch.bfloat16)
+    return w * torch.exp2(s).repeat_interleave(32, -1)
+
+
+def _offsets(sizes):
+    return torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+
+
+def _nan(*shape, f32):
+    return torch.full(shape, float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+
+
+def _same(y, ref):
+    ref = ref.to(y.dtype)   # an exact sum, rounded once
+    bad = ~(y == ref)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} differ, first at {bad.nonzero()[0].tolist()}: {y[bad][0]} for {ref[bad][0]}"
+
+
+def _mx_gemm_is_exact(M, N, K, xmx, seed=0):
+    X, W = _rows(M, K, seed), _weights(1, N, K, seed + 1)[0]
+    Wm = uw.uw_mx_quantize(W)
+    assert torch.equal(uw.uw_mx_dequantize(Wm), W)
+    ref = X.double() @ W.double().T
+    for f32 in (True, False):
+        _same(uw.uw_mx_gemm(uw.uw_mx_quantize(X) if xmx else X, Wm, out=_nan(M, N, f32=f32), out_f32=f32), ref)
+        assert uw.uw_last_device_status() == 0
+
+
+def _grouped_is_exact(sizes, N, K, mx, up, gather, seed=0):
+    E, R = len(sizes), int(sum(sizes))
+    T = max(1, R // 3) if gather else R
+    X = _rows(T, K, seed, 2.0 ** -6 if up else 1.0)
+    rows = torch.randint(0, T, (R,), generator=_gen(seed), device="cuda").int() if gather else None
+    W = [_weights(E, N, K, seed + 2 + 2 * i) for i in range(2 if up else 1)]
+    off = _offsets(sizes)
+    y = uw.uw_gemm_grouped(X, uw.uw_mx_quantize(W[0]) if mx else W[0], off, rows=rows,
+                           up=(uw.uw_mx_quantize(W[1]) if mx else W[1]) if up else None, out=_nan(R, N, f32=True), out_f32=True)
+    assert uw.uw_last_device_status() == 0
+    Xs = (X if rows is None else X[rows.long()]).double()
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        g, *u = [Xs[lo:hi] @ w[e].double().T for w in W]
+        if up:   # exact sums through the SwiGLU
+            zero = torch.zeros_like(g)
+            U.check(y[lo:hi], U.swiglu_ref(g, u[0]), U.swiglu_tolerance(g, u[0], zero, zero))
+        else:
+            _same(y[lo:hi], g)
+
+
+# ---------------------------------------------------------------- few tiles left over, few k steps
+@pytest.mark.parametrize("M,N,K,xmx", [(337, 14336, 4096, False), (400, 14336, 4096, False), (448, 14336, 4096, False),
+                                       (1500, 4096, 4096, False), (150, 9728, 2560, False), (112, 85, 2560, False),
+                                       (256, 28672, 8192, True), (375, 9626, 6976, True)])
+def test_mx_gemm_parts_of_few_steps(M, N, K, xmx):
+    _mx_gemm_is_exact(M, N, K, xmx)
+
+
+@pytest.mark.parametrize("sizes,N,K,up", [([256], 256, 2048, False), ([256], 19200, 4096, False), ([130, 0, 126], 9472, 2048, False),
+                                          ([130, 126], 4800, 2048, True)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_grouped_parts_of_few_steps(sizes, N, K, up, mx):
+    _grouped_is_exact(sizes, N, K, mx, up, True)
