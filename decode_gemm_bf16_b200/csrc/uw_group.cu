@@ -798,6 +798,19 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                     }
                 }
             }
+            // The MMAs' last commits arrive on barriers of both CTAs of a pair, and the second CTA would not wait for
+            // them otherwise: a CTA that left first would have them reach shared memory that it no longer owns.  So the
+            // ring is walked once more (a slot never used passes at once), then the final commit is waited for.
+            for (int i = 0; ok && i < p.S; i++) {
+                ok = wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag);
+                fb += 8;
+                if (++slot == p.S) {
+                    slot = 0;
+                    ph ^= 1u;
+                    fb = full;
+                }
+            }
+            if (rank) mbar_wait(fin, 0, 4 * p.timeout, nullptr);   // (the first CTA commits it on every path)
             if (!ok && rank == 0)   // every load already issued lands before the CTA (or the pair) exits
                 for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
                     mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
@@ -1167,7 +1180,9 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();   // no CTA leaves while the other's MMAs or arrivals reach it
+    // No CTA leaves while the other's MMAs or arrivals reach it: the commits' arrivals have been waited for (kProd), the
+    // warps' are ordered by this barrier.
+    if (CG == 2) cluster_sync();
     if (*abort_flag && threadIdx.x == 0) raise_status(UW_ERR_TIMEOUT);
     if (warp == kMma) {
         tc_fence_after();

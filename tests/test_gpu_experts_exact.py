@@ -95,3 +95,30 @@ def test_mx_gemm_parts_of_few_steps(M, N, K, xmx):
 @pytest.mark.parametrize("mx", [False, True])
 def test_grouped_parts_of_few_steps(sizes, N, K, up, mx):
     _grouped_is_exact(sizes, N, K, mx, up, True)
+
+
+# ---------------------------------------------------------------- pairs of CTAs that have nothing to do
+@pytest.mark.parametrize("M,N,K,xmx", [(100, 40, 128, False), (65, 300, 2048, False), (1, 64, 64, True), (200, 520, 512, True)])
+def test_most_pairs_idle(M, N, K, xmx):
+    """A tile or a few among 74 pairs, call after call: a pair leaves right after it has started."""
+    X, W = _rows(M, K, 1), _weights(1, N, K, 2)[0]
+    Xq, Wm = uw.uw_mx_quantize(X) if xmx else X, uw.uw_mx_quantize(W)
+    out = _nan(M, N, f32=True)
+    for i in range(600):
+        if i % 100 == 0:
+            out.fill_(float("nan"))
+        uw.uw_mx_gemm(Xq, Wm, out=out, out_f32=True)
+    _same(out, X.double() @ W.double().T)
+
+
+def test_most_pairs_idle_bf16():
+    _grouped_is_exact([0, 70, 0, 65], 200, 320, False, False, False)
+    X, W, off = _rows(135, 320, 1), _weights(4, 200, 320, 2), _offsets([0, 70, 0, 65])
+    y = uw.uw_gemm_grouped(X, W, off, out_f32=True)
+    for _ in range(600):
+        z = uw.uw_gemm_grouped(X, W, off, out_f32=True)
+    assert torch.equal(y, z)
+    empty = _offsets([0, 0, 0, 0])    # no pair has a tile
+    for _ in range(200):
+        out = uw.uw_gemm_grouped(X, W, empty, out=y, out_f32=True)
+    assert torch.equal(out, z)
