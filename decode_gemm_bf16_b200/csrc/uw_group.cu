@@ -77,7 +77,7 @@ namespace {
 constexpr int kTileN = 128;            // weight rows of a tile
 constexpr int kProd = 8, kMma = 9, kRebuild0 = 12, kRebuildWarps = 8;
 constexpr int kEpiWarps = 8;           // two per quarter of tensor memory's lanes
-constexpr int kMix = 10, kMix2 = 12;    // kGroupMx8: warps that join the scales of two weights, every other stage each
+constexpr int kMix = 10, kMix2 = 12;    // kGroupMx8: warps that join the scales of two weights, every other slot each
 constexpr int kRows = 11;              // TMA producer of X
 constexpr int kThreadsPlain = 12 * 32, kThreadsMix = 13 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
@@ -954,18 +954,18 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         // The tile's 128 rows are 64 of W and 64 of `up`, halves of a 128-row
         // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
         // either into the 16 bytes that tensor memory takes for lane l.  A stage
-        // costs a warp some 450 cycles of latency, so two take turns (8 experts of
+        // costs a warp some 450 cycles of latency, so two share the slots (8 experts of
         // 14336 x 4096 twice, 16 rows: 96 us, 108 with one).
         if (p.up) {
-            int turn = warp == kMix ? 0 : 1;
+            const int mine = warp == kMix ? 0 : 1;
             Walk wk(work, worker);
             Seg sg;
             Ring r;
             bool ok = true;
             Tile t;
             while (ok && wk.next(p, tl, pl, sg, t)) {
-                for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S), turn ^= 1) {
-                    if (turn) continue;
+                for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
+                    if (slot_warp(r.i) != mine) continue;
                     if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
                     const uint32_t at = ss + (uint32_t)(lane * 16 + ((t.n * CG + rank) & 1) * 8);

@@ -118,4 +118,10 @@ UW_HD uint32_t last_joined(const Plan& pl, const Seg& s, uint32_t b) {
     return pl.parts ? b + (pl.parts - 1) * pl.rest : unit_owner((s.tile - pl.whole + 1) * pl.kt - 1, pl);
 }
 
+// Two warps share the work on a ring's slots.  A slot always has the same warp:
+// a wait on a parity tells a phase from the one before alone, so whoever waits
+// for a slot has to have seen its last phase too.  (Taking stages in turn, as
+// it was, changes a slot's warp on every wrap of a ring of odd length.)
+UW_HD int slot_warp(int slot) { return slot & 1; }
+
 }  // namespace uw

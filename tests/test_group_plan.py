@@ -68,6 +68,8 @@ extern "C" int check_plan(uint32_t tiles, uint32_t P, uint32_t kt, uint32_t acc_
     return 0;
 }
 
+extern "C" int warp_of_slot(int slot) { return slot_warp(slot); }
+
 // The first (tiles, kt) in the ranges whose plan is not sound.
 extern "C" int sweep(uint32_t tiles0, uint32_t tiles1, uint32_t P, uint32_t kt0, uint32_t kt1, uint32_t acc_w, int cut_parts,
                      uint32_t* bad) {
@@ -137,3 +139,16 @@ def test_both_sides_of_the_limits(L):
     for cut in (0, 1):
         p = _plan(L, 296, 148, 256, 256, cut)
         assert p["whole"] == 296 and not p["ps"] and not p["parts"]
+
+
+def _seen_before(warp_of_stage, S, stages=200):
+    """Whether every wait for a slot is made by a warp that has seen the slot's phase before (a wait on a parity cannot
+    tell a phase from the last but one)."""
+    return all(warp_of_stage(q) == warp_of_stage(q - S) for q in range(S, stages))
+
+
+@pytest.mark.parametrize("S", range(2, 13))
+def test_a_slot_keeps_its_warp(L, S):
+    assert _seen_before(lambda q: L.warp_of_slot(q % S), S)
+    assert {L.warp_of_slot(q % S) for q in range(S)} == {0, 1}
+    assert _seen_before(lambda q: q % 2, S) == (S % 2 == 0)   # stages in turn: wrong for every odd ring
