@@ -77,7 +77,7 @@ namespace {
 constexpr int kTileN = 128;            // weight rows of a tile
 constexpr int kProd = 8, kMma = 9, kRebuild0 = 12, kRebuildWarps = 8;
 constexpr int kEpiWarps = 8;           // two per quarter of tensor memory's lanes
-constexpr int kMix = 10, kMix2 = 12;    // kGroupMx8: warps that join the scales of two weights, every other slot each
+constexpr int kMix = 10, kMix2 = 12;    // kGroupMx8, single CTAs: warps that join the scales of two weights, every other slot each
 constexpr int kRows = 11;              // TMA producer of X
 constexpr int kThreadsPlain = 12 * 32, kThreadsMix = 13 * 32;
 constexpr int kThreadsRebuild = (kRebuild0 + kRebuildWarps) * 32;
@@ -93,7 +93,7 @@ constexpr uint32_t kTmemCols = 512;
 struct Maps {
     CUtensorMap x;        // rows of X (or, split rows, 16 prepared rows a box)
     CUtensorMap w, u;     // weights
-    CUtensorMap sw;       // W's scale tiles, 512 bytes a row (pairs)
+    CUtensorMap sw;       // W's scale tiles, or the joined ones of W and `up`, 512 bytes a row (pairs)
     CUtensorMap sx;       // X's (pairs; split rows: the scales in front of the prepared rows)
 };
 
@@ -492,9 +492,8 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
     return a;
 }
-// arrive_at itself orders nothing: the scales that kMix wrote are ordered by
-// its fence to the proxy that reads them.  (A release at cluster scope costs
-// about 1600 cycles, three stages' time.)
+// arrive_at orders no writes: it is for the accumulator's release alone, where
+// there are none to order (see `release`).
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -564,7 +563,7 @@ __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, uint64_
 // What the producer thread loads for the stages of one tile, from k step kt on:
 // everything that changes from stage to stage is advanced, not computed anew.
 // In a pair every load counts on the first CTA's barrier, which expects the
-// bytes of both; only the scales that kMix joins have a barrier in each CTA.
+// bytes of both.
 template <int SRC, int CG>
 struct Feed {
     static constexpr int KB = stage_k(SRC);
@@ -595,7 +594,7 @@ struct Feed {
         x_bytes = SRC == kGroupMx8 && CG == 1 ? (uint32_t)nN * 128u : gathers ? (uint32_t)gathers * 512u : (uint32_t)(boxes * p.box) * 128u;
         // the unpacking load counts the packed bytes of its rows
         tx = (uint32_t)kTileN * (SRC == kGroupMx8 ? 64u : kARow) + p.sf_b_bytes + x_bytes;
-        if (!joined(p)) tx += p.sf_a_bytes * (p.up ? 2u : 1u);
+        tx += p.sf_a_bytes * (p.up && CG == 1 ? 2u : 1u);
         tx *= CG;
         s0 = s1 = x0 = x1 = nullptr;
         sy = half = xy0 = xy1 = 0;
@@ -608,7 +607,7 @@ struct Feed {
             half = kt & 1;
             s0 = p.sw + at * (kMxTileBytes / 2);
             if (p.up) s1 = p.su + at * (kMxTileBytes / 2);
-            sy = (int)at;
+            sy = joined(p) ? (int)((2 * (t.e * p.w_row_tiles + t.n) + rank) * p.kt + kt) : (int)at;
         }
         if (SRC == kGroupMx8) {
             const int64_t chunk = t.m * p.kt + kt;
@@ -626,18 +625,12 @@ struct Feed {
             xy1 = (int)(2 * a1);
         }
     }
-    // scales of two weights, joined by kMix
+    // scales of two weights, joined before this kernel: loaded with X, behind the wait for what the preparing kernel writes
     __device__ static __forceinline__ bool joined(const GroupParams& p) { return SRC == kGroupMx8 && CG == 2 && p.up; }
 
-    // `lb`: the stage's barrier here, `fb`: the one that counts (pairs: the first CTA's), `sb`: that of the scales to be joined
-    __device__ __forceinline__ void weights(const GroupParams& p, const Maps& m, uint32_t st, uint32_t lb, uint32_t fb, uint32_t sb,
-                                            bool expect) {
+    // `lb`: the stage's barrier here, `fb`: the one that counts (pairs: the first CTA's)
+    __device__ __forceinline__ void weights(const GroupParams& p, const Maps& m, uint32_t st, uint32_t lb, uint32_t fb, bool expect) {
         if (expect) mbar_arrive_expect_tx(lb, tx);
-        if (joined(p)) {
-            mbar_arrive_expect_tx(sb, 2u * p.sf_a_bytes);
-            bulk_load(st + p.off_s, s0, p.sf_a_bytes, sb);
-            bulk_load(st + p.off_s + p.sf_a_bytes, s1, p.sf_a_bytes, sb);
-        }
         load_box<CG>(st, &m.w, ax, w0, fb);
         load_box<CG>(st + kTileN / 2 * kARow, second, ax, w1, fb);
         ax += SRC == kGroupBf16 || SRC == kGroupMx8 ? KB : KB / 2;
@@ -661,6 +654,7 @@ struct Feed {
                 bulk_load(st + p.off_b - p.sf_b_bytes, x0, p.sf_b_bytes + x_bytes, fb);
                 x0 += p.prep_chunk;
             } else {         // all columns' scales, this CTA's half of the rows
+                if (p.up) tma_load_pair(st + p.off_s, &m.sw, 0, sy++, fb);
                 tma_load_pair(st + p.off_b - p.sf_b_bytes, &m.sx, 0, xy0, fb);
                 for (int b = 0; b < boxes; b++) tma_load_pair(st + p.off_b + (uint32_t)(b * p.box) * 128u, &m.x, 0, xy1 + b * p.box, fb);
                 xy0 += (int)(p.prep_chunk / 128);
@@ -702,8 +696,8 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ctrl_off);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxS, recon = empty + 8 * kMaxS, tfree = recon + 8 * kMaxT;
-    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8, joins = mixed + 8 * kMaxS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * kMaxS + 2 * kMaxT + 5);
+    const uint32_t accf = tfree + 8 * kMaxT, acce = accf + 16, fin = acce + 16, mixed = fin + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxS + 2 * kMaxT + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* cum = reinterpret_cast<int32_t*>(smem + p.tab_off);
     int32_t* begin = cum + p.E + 1;
@@ -722,8 +716,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         if (lane < p.S) {
             mbar_init(full + 8 * lane, 1);
             mbar_init(empty + 8 * lane, 1);
-            mbar_init(joins + 8 * lane, 1);
-            mbar_init(mixed + 8 * lane, CG);
+            mbar_init(mixed + 8 * lane, 1);
         }
         if (kRe && lane < p.T) {
             mbar_init(recon + 8 * lane, kRebuildWarps);
@@ -787,7 +780,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 Feed<SRC, CG> f(p, m, t, sg.kt0, rank);
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, q++) {
                     if (!wait_one(fb + 8 * kMaxS, ph, p.timeout, abort_flag)) { ok = false; break; }   // empty
-                    f.weights(p, m, st, fb, fb + sig, fb + (joins - full), rank == 0);
+                    f.weights(p, m, st, fb, fb + sig, rank == 0);
                     st += p.stage_bytes;
                     fb += 8;
                     if (++slot == p.S) {
@@ -883,9 +876,9 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             uint32_t more = 0;   // 0: the tile's first MMA overwrites
             for (int kt = sg.kt0; kt < sg.kt1; kt++) {
                 if (kRe && !wait_one(recon + 8 * rt.i, rt.ph, p.timeout, abort_flag)) { ok = false; break; }
-                if (SRC == kGroupMx8 && p.up && !wait_pair<CG>(fb + (mixed - full), ph, p.timeout, abort_flag)) { ok = false; break; }
-                // (one CTA: joined scales come after everything else of the stage)
-                if (!(SRC == kGroupMx8 && CG == 1 && p.up) && !wait_one(fb, ph, p.timeout, abort_flag)) { ok = false; break; }
+                // (scales joined on chip come after everything else of the stage)
+                const uint32_t ready = SRC == kGroupMx8 && CG == 1 && p.up ? fb + (mixed - full) : fb;
+                if (!wait_one(ready, ph, p.timeout, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (kScaled) {
                     // scales of the stage, 4 columns per 512 bytes: weights, then rows
@@ -906,7 +899,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                             tc_mma_mx<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
                                       sf + 4u * (j >> 1), sfx + 4u * nb * (j >> 1), more);
                     } else {
-                        tc_copy_scales<CG>(sf, p.up ? ss + 64u : ss);
+                        tc_copy_scales<CG>(sf, CG == 1 && p.up ? ss + 64u : ss);
                         tc_copy_scales<CG>(sfb, sb);
                         if (p.sf_b_bytes > 512u) tc_copy_scales<CG>(sfb + 4u, sb + 32u);
 #pragma unroll
@@ -949,11 +942,14 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
         mbar_wait(fin, 0, p.timeout, nullptr);
         }
         __syncwarp();
-    } else if (SRC == kGroupMx8 && (warp == kMix || warp == kMix2)) {
+    } else if (SRC == kGroupMx8 && CG == 1 && (warp == kMix || warp == kMix2)) {
         // ------------------------------------------------------------ scales of two weights
         // The tile's 128 rows are 64 of W and 64 of `up`, halves of a 128-row
         // scale tile each: lane l joins the 8 bytes of its rows l and l + 32 of
-        // either into the 16 bytes that tensor memory takes for lane l.  A stage
+        // either into the 16 bytes that tensor memory takes for lane l.  (Pairs find
+        // them joined in the workspace: what the second CTA's warps write would have
+        // to be released to the first's MMAs at cluster scope, about 1600 cycles a
+        // stage.)  A stage
         // costs a warp some 450 cycles of latency, so two share the slots (8 experts of
         // 14336 x 4096 twice, 16 rows: 96 us, 108 with one).
         if (p.up) {
@@ -966,9 +962,9 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             while (ok && wk.next(p, tl, pl, sg, t)) {
                 for (int kt = sg.kt0; kt < sg.kt1; kt++, r.advance(p.S)) {
                     if (slot_warp(r.i) != mine) continue;
-                    if (!mbar_wait((CG == 2 ? joins : full) + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait(full + 8 * r.i, r.ph, p.timeout, abort_flag)) { ok = false; break; }
                     const uint32_t ss = base + (uint32_t)r.i * p.stage_bytes + p.off_s;
-                    const uint32_t at = ss + (uint32_t)(lane * 16 + ((t.n * CG + rank) & 1) * 8);
+                    const uint32_t at = ss + (uint32_t)(lane * 16 + (t.n & 1) * 8);
                     const uint32_t to = ss + 1024u + (uint32_t)(lane * 16);
 #pragma unroll
                     for (uint32_t i = 0; i < 2; i++) {
@@ -977,10 +973,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 2) arrive_at(in_first(mixed + 8 * r.i));
-                        else mbar_arrive(mixed + 8 * r.i);
-                    }
+                    if (lane == 0) mbar_arrive(mixed + 8 * r.i);
                 }
             }
         }
@@ -1047,9 +1040,10 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
             if (any_of_epilogue(!good)) break;
             tc_fence_after();
             const uint32_t acc = trow + (uint32_t)ra.i * p.acc_w;
-            // The accumulator is free once this warp has read its share.  (An arrival in the pair's first CTA orders nothing by
-            // itself: the loads are complete, which is all that the MMAs that overwrite it need.  At cluster scope a release
-            // would cost about 1600 cycles a tile.)
+            // The accumulator is free once this warp has read its share.  Nothing was written that the MMAs which overwrite it
+            // would read, so a relaxed arrival at cluster scope will do: it is the form that the PTX manual gives for a
+            // tcgen05.ld before another thread's tcgen05.mma (wait::ld, fence::before_thread_sync, relaxed arrive; wait,
+            // fence::after_thread_sync, mma).
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -1191,7 +1185,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 }
 
 template <int SRC, int CG>
-__global__ void __launch_bounds__(SRC == kGroupMx8 ? kThreadsMix : kThreadsPlain, 1)
+__global__ void __launch_bounds__(SRC == kGroupMx8 && CG == 1 ? kThreadsMix : kThreadsPlain, 1)
     k_group(const __grid_constant__ Maps m, const GroupParams p) {
     group_body<SRC, CG>(m, p);
 }
@@ -1212,6 +1206,10 @@ struct PrepParams {
     uint32_t sf_bytes;        // scale bytes in front of a stage's rows
     int64_t chunk;
     uint8_t* out;
+    const uint8_t* sw;        // scale tiles of two weights to be joined
+    const uint8_t* su;
+    uint8_t* joined;          // NULL: not wanted
+    int row_tiles, k_tiles;   // of one matrix
 };
 
 constexpr int kPrepThreads = 256;
@@ -1324,6 +1322,31 @@ __device__ __forceinline__ Split16 split16(const uint4 a, const uint4 b) {
     return q;
 }
 
+// Scales of W and `up` for a pair of CTAs, each with 64 rows of either: of the
+// 16 bytes that a half scale tile holds for lane l (rows l, l + 32, l + 64, l +
+// 96) the first CTA takes the first 8 of W and of `up`, the second the last 8.
+// Row ((expert, 64 weight rows), k step) of `joined` is 512 bytes.  A warp joins
+// one scale tile of either weight at a time; bound by reading and writing one
+// byte per 32 weights.
+__device__ __forceinline__ void join_scales(const PrepParams& p, const int32_t* count, uint32_t w0, uint32_t warps) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t per = (uint32_t)(p.row_tiles * p.k_tiles), items = (uint32_t)p.E * per;   // (below 2^31: one CTA quantises a tile)
+    for (uint32_t i = w0; i < items; i += warps) {
+        const uint32_t e = i / per, t = i - e * per, rt = t / (uint32_t)p.k_tiles, kt = 2u * (t - rt * (uint32_t)p.k_tiles);
+        if (!count[e]) continue;   // no tile reads them
+        const uint4* w = reinterpret_cast<const uint4*>(p.sw + (int64_t)i * kMxTileBytes) + lane;
+        const uint4* u = reinterpret_cast<const uint4*>(p.su + (int64_t)i * kMxTileBytes) + lane;
+        const uint4 a[2] = {__ldg(w), __ldg(w + 32)}, b[2] = {__ldg(u), __ldg(u + 32)};
+        uint4* out = reinterpret_cast<uint4*>(p.joined) + (2 * ((int64_t)e * p.row_tiles + rt) * p.kt + kt) * 32 + lane;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (kt + h >= (uint32_t)p.kt) break;   // K an odd multiple of 128
+            out[h * 32] = make_uint4(a[h].x, a[h].y, b[h].x, b[h].y);
+            out[((int64_t)p.kt + h) * 32] = make_uint4(a[h].z, a[h].w, b[h].z, b[h].w);
+        }
+    }
+}
+
 // Rows of split tiles.  A warp takes `steps` (1 or 2) times 512 k of one slot
 // at a time, 16 values a lane and step, two lanes a block of 32; slots are
 // dealt out evenly whatever the groups are.  Row r of a tile of n (rounded up
@@ -1351,6 +1374,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParam
     const uint32_t w0 = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
     const int unit = lane & 7;   // 16-byte unit of the stage's row
     bool wrong = false;
+    if (p.joined) join_scales(p, count, w0, warps);
     uint32_t seg = w0 % segs;
     for (uint32_t s = s_first + w0 / segs; s < s_end;) {
         int64_t row = s;
@@ -1457,8 +1481,8 @@ bool pick_parts(int CG) { return CG == 2; }
 
 constexpr size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// How a call is cut up; the workspace holds partial sums, their tags, and the
-// prepared rows.
+// How a call is cut up; the workspace holds partial sums, their tags, the
+// prepared rows and the joined scales.
 struct Shape {
     int MG = 0, KB = 0, kt = 0, n_tiles = 0;
     int CG = 1;               // CTAs of a worker
@@ -1466,8 +1490,8 @@ struct Shape {
     bool gather = false;      // a gathered copy of BF16 rows
     uint32_t sf_b = 0;        // scale bytes of a stage's rows
     int64_t chunk = 0;        // split rows: bytes of a stage
-    size_t partial = 0, flags = 0, prep = 0;
-    size_t bytes() const { return partial + flags + prep; }
+    size_t partial = 0, flags = 0, prep = 0, joined = 0;
+    size_t bytes() const { return partial + flags + prep + joined; }
 };
 
 Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, bool rows) {
@@ -1486,6 +1510,7 @@ Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, boo
         h.sf_b = 512u * (uint32_t)((2 * h.MG + 127) / 128);
         h.chunk = (int64_t)h.sf_b + 2 * h.MG * 128;
         h.prep = al256((size_t)h.m_tiles * h.kt * h.chunk);
+        if (up && h.CG == 2) h.joined = (size_t)E * 2 * (size_t)mx_row_tiles(N) * (size_t)h.kt * (kMxTileBytes / 2);
     } else if (src == kGroupMxMx) {
         h.sf_b = (uint32_t)mx_row_tiles(h.MG) * kMxTileBytes;
     } else if (rows && h.MG > 32) {
@@ -1574,8 +1599,8 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.off_s = kTileN * (src == kGroupMx ? 32u : 128u);
     p.sf_a_bytes = src == kGroupBf16 ? 0 : src == kGroupMxMx ? kMxTileBytes : kMxTileBytes / 2;
     p.sf_b_bytes = h.sf_b;
-    // (with `up`, split rows: a third part for the joined scales of both weights)
-    p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up ? (src == kGroupMx8 ? 3 : 2) : 1) + p.sf_b_bytes);
+    // (with `up`, split rows and a single CTA: a third part for the joined scales of both weights; pairs load them joined)
+    p.off_b = al1k(p.off_s + p.sf_a_bytes * (p.up && CG == 1 ? (src == kGroupMx8 ? 3 : 2) : 1) + p.sf_b_bytes);
     p.stage_bytes = p.off_b + (uint32_t)(MG * 128 * (src == kGroupMx8 ? 2 : 1) / CG);
     const uint32_t ctrl = 1024, tab = (uint32_t)(3 * a.E + 1) * 4;
     const uint32_t epi = kEpiWarps * kWarpStage + (p.up ? kExchange : 0);
@@ -1631,7 +1656,10 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
             ok = ok && make_map_2d(mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.K / 2, wrows, a.K / 2, src == kGroupMx ? 32 : 128,
                                    kTileN / 2, src == kGroupMx ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B);
     }
-    if (CG == 2 && src != kGroupBf16 && !a.up)
+    uint8_t* joined = h.joined ? prep + h.prep : nullptr;
+    if (joined)
+        ok = ok && make_map_2d(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, joined, 128, h.joined / 512, 512, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+    else if (CG == 2 && src != kGroupBf16)
         ok = ok && make_map_2d(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.w_scales, 128, 2 * (uint64_t)a.E * p.w_row_tiles * p.k_tiles,
                                512, 128, halves, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) { *st = UW_ERR_CUDA; return cudaSuccess; }
@@ -1664,7 +1692,13 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
             // warps take two steps at a time where that leaves none idle
             const int64_t one = a.slots * ((a.K + kPrepK - 1) / kPrepK), most = 4 * (int64_t)P;
             q.steps = one > 2 * most * (kPrepThreads / 32) ? 2 : 1;
-            const int64_t ctas = (one / q.steps + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+            q.sw = a.w_scales;
+            q.su = a.up_scales;
+            q.joined = joined;
+            q.row_tiles = (int)p.w_row_tiles;
+            q.k_tiles = p.k_tiles;
+            const int64_t items = joined ? a.E * p.w_row_tiles * p.k_tiles : 0;
+            const int64_t ctas = ((one / q.steps > items ? one / q.steps : items) + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
             e = launch_after(k_group_split, dim3((unsigned)(ctas < most ? ctas : most)), 1, kPrepThreads, tab + (size_t)a.E * 4, s, q);
         } else {
             e = launch_after(k_group_gather, dim3((unsigned)(a.slots < 8 * P ? a.slots : 8 * P)), 1, kPrepThreads, 0, s, q);
@@ -1673,7 +1707,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     }
     const int64_t workers = max_tiles * h.kt < P / CG ? max_tiles * h.kt : P / CG;
     return launch_after(kern, dim3((unsigned)(workers * CG)), CG,
-                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 && p.up ? kThreadsMix : kThreadsPlain, smem, s, m, p);
+                        src == kGroupMx ? kThreadsRebuild : src == kGroupMx8 && CG == 1 && p.up ? kThreadsMix : kThreadsPlain, smem, s, m, p);
 }
 
 }  // namespace uw

@@ -122,3 +122,18 @@ def test_most_pairs_idle_bf16():
     for _ in range(200):
         out = uw.uw_gemm_grouped(X, W, empty, out=y, out_f32=True)
     assert torch.equal(out, z)
+
+
+# ---------------------------------------------------------------- scales of two weights
+@pytest.mark.parametrize("sizes,N,K", [([130, 70, 0, 200], 200, 384), ([100] * 5, 64, 128), ([300], 1000, 2048), ([0, 90, 85], 129, 1152),
+                                       ([20, 30], 200, 1152), ([1, 2, 3], 328, 2048), ([60, 50], 1408, 640)])
+def test_scales_of_gate_and_up(sizes, N, K):
+    """Blocks of 32 weights scaled by 1, 2 or 4 at random, in gate and in up: single CTAs and pairs, rings of odd length,
+    an odd multiple of 128 along K, half a scale tile of rows, experts without slots."""
+    for seed in range(3):
+        _grouped_is_exact(sizes, N, K, True, True, seed % 2 == 0, seed=100 * seed)
+
+
+def test_many_stages_of_gate_and_up():
+    _grouped_is_exact([40] * 16, 704, 4096, True, True, True, seed=5)
+    _grouped_is_exact([180, 230, 97, 400], 1408, 4096, True, True, True, seed=6)
