@@ -63,6 +63,7 @@
 //   both in 4 bits, 2048 rows of 14336 x 4096: 51 us, 4.7 PFLOP/s; 8192^3: 192
 //     us, 5.7 PFLOP/s.
 #include <cuda_fp16.h>
+#include <cstdlib>
 
 #include "uw_device.cuh"
 #include "uw_internal.h"
@@ -88,6 +89,7 @@ constexpr int kEpiBarId = 1;
 constexpr uint32_t kWarpStage = 2048;  // transpose buffer of an epilogue warp
 constexpr uint32_t kExchange = kEpiWarps * 2048;   // `up`: 16 slots x 32 rows of fp32 sums a warp
 constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kRestNs = 1000000;  // after an expired wait: see the kernel's end
 
 // Tensor maps of a call (unused ones are left empty).
 struct Maps {
@@ -124,6 +126,7 @@ struct GroupParams {
     float* partial;                         // [CTAs][MG/4][128] float4
     unsigned long long* flags;              // [CTAs][8]: call tag once a warp's partial sums are out
     unsigned long long epoch;
+    unsigned long long tag;                 // what is written there: the epoch (but for a test of the limit)
     uint64_t timeout;
 };
 
@@ -804,9 +807,15 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 }
             }
             if (rank) mbar_wait(fin, 0, 4 * p.timeout, nullptr);   // (the first CTA commits it on every path)
-            if (!ok && rank == 0)   // every load already issued lands before the CTA (or the pair) exits
-                for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++)
-                    mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), p.timeout, nullptr);
+            // On expiry the loads of the last stages land before the CTA (or the pair) exits.  (All of them within one
+            // limit: a stage of which another thread issued no part never completes.)
+            if (!ok && rank == 0) {
+                const uint64_t end = globaltimer() + p.timeout;
+                for (int64_t qq = q - p.S < 0 ? 0 : q - p.S; qq < q; qq++) {
+                    const uint64_t t0 = globaltimer();
+                    mbar_wait(full + 8 * (uint32_t)(qq % p.S), (uint32_t)((qq / p.S) & 1), t0 < end ? end - t0 : 0, nullptr);
+                }
+            }
         }
         __syncwarp();
     } else if (warp == kRows) {
@@ -1080,7 +1089,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                 release();   // (synchronises the warp: the tag's release covers every lane's stores)
                 if (lane == 0)
                     asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.flags + (size_t)(worker * CG + rank) * kEpiWarps + warp),
-                                 "l"(p.epoch)
+                                 "l"(p.tag)
                                  : "memory");
             } else {
                 // 16 slots of the finished sum: the accumulator plus the other ranges' partial sums, in k order
@@ -1174,6 +1183,10 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 
     tc_fence_before();
     __syncthreads();
+    // On expiry a role may have issued loads for a stage that the others did not come to; no barrier shows when these
+    // have landed, so they are given a thousand times a load's latency.  (Nothing is issued any more.)
+    if (*abort_flag)
+        for (const uint64_t end = globaltimer() + kRestNs; globaltimer() < end;) {}
     // No CTA leaves while the other's MMAs or arrivals reach it: the commits' arrivals have been waited for (kProd), the
     // warps' are ordered by this barrier.
     if (CG == 2) cluster_sync();
@@ -1520,6 +1533,17 @@ Shape shape_of(int src, int64_t slots, int E, int64_t N, int64_t K, bool up, boo
     return h;
 }
 
+// Test hook (UW_DEBUG_SKIP_TAGS=1, read once): cut tiles' partial sums are
+// published under a tag that nobody waits for, so that the wait for them runs
+// out.
+bool skip_tags() {
+    static const bool skip = [] {
+        const char* e = getenv("UW_DEBUG_SKIP_TAGS");
+        return e && e[0] == '1';
+    }();
+    return skip;
+}
+
 // The unpacking TMA load takes rows of whole 128 codes.
 int resolve(int src, int64_t K) { return src == kGroupMx && K % 128 == 0 ? kGroupMx8 : src; }
 
@@ -1592,6 +1616,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.partial = (float*)a.ws;
     p.flags = (unsigned long long*)((uint8_t*)a.ws + h.partial);
     p.epoch = gemm_next_epoch();
+    p.tag = skip_tags() ? ~0ull : p.epoch;   // (an epoch has 48 bits)
     p.timeout = timeout_ns();
 
     // stage: weight rows, their scales, the rows' scales, X (swizzled tiles 1024-byte aligned)

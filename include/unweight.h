@@ -476,7 +476,12 @@ uw_status uw_route(const void* logits, int in_f32, int64_t T, int E, int k, int 
  *     K up to about 6 million.
  *   Y: device [slots, N], BF16 or float32 (out_f32), 16-byte aligned.
  *   workspace: 256-byte aligned, any contents, owned by the call until it
- *     completes (a captured call owns it whenever its graph runs). */
+ *     completes (a captured call owns it whenever its graph runs).  After
+ *     UW_ERR_TIMEOUT a captured call's workspace has to be cleared before its
+ *     graph runs again: it may hold tags of the run that gave up.
+ * For testing the limit of the waits, UW_DEBUG_SKIP_TAGS=1 (environment, read
+ * once) makes products that cut tiles along k, uw_mx_gemm's too, wait for sums
+ * that nobody publishes: UW_ERR_TIMEOUT after UW_TIMEOUT_MS. */
 typedef struct {
     const uint16_t* X;
     int64_t x_rows;

@@ -137,3 +137,40 @@ def test_scales_of_gate_and_up(sizes, N, K):
 def test_many_stages_of_gate_and_up():
     _grouped_is_exact([40] * 16, 704, 4096, True, True, True, seed=5)
     _grouped_is_exact([180, 230, 97, 400], 1408, 4096, True, True, True, seed=6)
+
+
+# ---------------------------------------------------------------- waits that run out
+_EXPIRED_CHILD = r"""
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import decode_gemm_bf16_b200 as uw
+from tests import test_gpu_experts_exact as E
+
+def product(M, N, K, mx, up):
+    X, W = E._rows(M, K, 1), E._weights(1, N, K, 2)
+    Wq = uw.uw_mx_quantize(W) if mx else W
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    y = uw.uw_gemm_grouped(X, Wq, off, up=Wq if up else None, out_f32=True)
+    return y, X.double() @ W[0].double().T
+
+for case in ((4, 640, 8192, False, False), (4, 640, 8192, True, False), (4, 640, 8192, True, True), (4, 640, 8256, True, False),
+             (256, 256, 4096, False, False), (200, 300, 8192, True, False), (200, 300, 8192, True, True)):
+    product(*case)                        # cut along k: the joining worker waits in vain
+    print("expired", uw.uw_last_device_status())
+    y, ref = product(100, 200, 128, case[3], False)   # too short to be cut
+    print("after", uw.uw_last_device_status(), int((y.double() == ref).all()))
+"""
+
+
+def test_waits_that_run_out_are_reported_and_harm_nothing():
+    """Partial sums that nobody publishes (the UW_DEBUG_SKIP_TAGS hook): single CTAs and pairs, BF16 and 4-bit weights, gate
+    and up, end with UW_ERR_TIMEOUT, and the next call is right.  In a child process: hook and limit stay out of the others."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, UW_TIMEOUT_MS="20", UW_DEBUG_SKIP_TAGS="1")
+    r = subprocess.run([sys.executable, "-c", _EXPIRED_CHILD, root], env=env, capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0, r.stderr[-3000:]
+    lines = r.stdout.strip().splitlines()
+    assert lines[0::2] == ["expired 7"] * 7 and lines[1::2] == ["after 0 1"] * 7, r.stdout
