@@ -744,9 +744,11 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     // With a preparing kernel before this one the offsets and weights are
     // complete already (see k_group_split); what it writes is waited for below.
     if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count);
+    // (not before this CTA has its tensor memory: a dependent CTA on the same SM that took it first would keep it while it
+    // waits for this kernel)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (CG == 2) cluster_sync();   // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -1649,7 +1651,9 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.stg_off = p.ctrl_off + ctrl;
     p.tab_off = p.stg_off + epi;
     p.work_off = p.tab_off + tab16;
-    const size_t smem = (size_t)S * p.stage_bytes + fixed;
+    // One CTA per SM: each takes all of its tensor memory, and two calls on two streams whose CTAs wait for each other's
+    // tensor memory and for their own grid's partial sums could stand still.
+    const size_t one_per_sm = 116 * 1024, used = (size_t)S * p.stage_bytes + fixed, smem = used > one_per_sm ? used : one_per_sm;
 
     Maps m{};
     bool ok = true;

@@ -174,3 +174,21 @@ def test_waits_that_run_out_are_reported_and_harm_nothing():
     assert r.returncode == 0, r.stderr[-3000:]
     lines = r.stdout.strip().splitlines()
     assert lines[0::2] == ["expired 7"] * 7 and lines[1::2] == ["after 0 1"] * 7, r.stdout
+
+
+def test_small_rebuilt_tiles_on_two_streams():
+    """K an odd multiple of 64 and few rows (the least shared memory of all forms), tiles cut along k, on two streams at once."""
+    cases = []
+    for seed, (M, N, K) in enumerate([(3, 700, 4160), (16, 900, 2112), (1, 2000, 8256)]):
+        X, W = _rows(M, K, seed), _weights(1, N, K, seed + 5)[0]
+        cases.append((X, uw.uw_mx_quantize(W), X.double() @ W.double().T))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(60):
+        for j, s in enumerate(streams):
+            X, W, ref = cases[(i + j) % 3]
+            with torch.cuda.stream(s):
+                got.append((uw.uw_mx_gemm(X, W, out_f32=True), ref))
+    torch.cuda.synchronize()
+    for y, ref in got:
+        _same(y, ref)
