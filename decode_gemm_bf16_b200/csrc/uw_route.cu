@@ -222,7 +222,9 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, bool in,
     uint32_t mine = 0;
     if (!F32) {
         mine = got & ~kLow;
-        if (mine) mine |= mine >> 31 ? 0u : kLow;   // a negative logit's key has its low bits set
+        // A BF16 logit's key ends in 16 zeros, a negative one's in 16 ones, and so does that of +infinity, which counts as
+        // the largest fp32 number: the softmax subtracts that very number.
+        if (mine & 0xFFFFu) mine |= kLow;
     } else {
         if (id >= 0) mine = bits_key(__ldg(reinterpret_cast<const uint32_t*>(p.logits) + t * p.E + id));
         if (__any_sync(kFull, edge)) {

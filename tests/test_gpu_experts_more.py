@@ -1,0 +1,68 @@
+"""Router logits at the ends of the range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_gemm_bf16_b200 as uw
+from tests import expert_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    assert uw.uw_last_device_status() == 0
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# ---------------------------------------------------------------- router
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,k", [(14, 48, 6), (200, 48, 6), (3000, 60, 4), (2500, 256, 8), (400, 300, 5), (40, 1000, 12)])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_route_ends_of_the_range(T, E, k, score, renorm, dtype):
+    """Infinities, the largest and the lowest number, masked and NaN logits: one CTA, a warp a token, eight lanes a token."""
+    x = (torch.randn(T, E, generator=_gen(T), device="cuda") * 2).to(dtype)
+    fin = torch.finfo(dtype)
+    x[torch.rand(T, E, generator=_gen(2), device="cuda") < 0.3] = -math.inf
+    for r, t in enumerate(range(0, T, 14)):       # (sets of rows, the last may be short)
+        rows = x[t:t + 14]
+        for i, row in enumerate(rows):
+            if i == 0:
+                row[9] = math.inf                 # all the weight
+            elif i == 1:
+                row[10:13] = math.inf             # equal shares
+            elif i == 2:
+                row[7], row[20] = fin.max, math.inf   # infinity is above every number
+            elif i == 3:
+                row[5:9] = fin.max
+            elif i == 4:
+                row[:] = fin.min
+            elif i == 5:
+                row[:] = -math.inf
+                row[3] = fin.min
+            elif i == 6:
+                row[:] = math.inf
+            elif i == 7:
+                row[:k] = math.nan
+            elif i == 8:
+                row[:] = math.nan
+                row[E - 1] = math.inf
+            elif i == 9:
+                row[:] = -math.inf
+    r = uw.uw_route(x, k, score=score, renorm=renorm)
+    ids, w, offsets, rows, pos = U.route_ref(x.double().cpu().numpy(), k, score, renorm, 1.0)
+    for got, want, name in ((r.ids, ids, "ids"), (r.offsets, offsets, "offsets"), (r.rows, rows, "rows"), (r.pos, pos, "pos")):
+        assert np.array_equal(got.cpu().numpy(), want), name
+    got = r.weights.double().cpu().numpy()
+    # finite logits that carry weight are within 32 of each other: exp off by 2 ulps, its argument by 2^-24 32; the sum of
+    # E terms by (E/32 + 5) 2^-24, divisions by 1; weights below the normal range by their spacing
+    assert np.isfinite(got).all()
+    assert (np.abs(got - w) <= (2 * 32 + 16 + E / 16) * 2.0 ** -24 * np.abs(w) + 2.0 ** -126).all(), float(np.abs(got - w).max())
