@@ -1166,7 +1166,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 #pragma unroll
                                 for (int i = i0; i < i0 + 8; i++) {
                                     const float g = __uint_as_float(first ? keep[i] : o[i]), u = __uint_as_float(first ? o[i] : keep[i]);
-                                    keep[i] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * u);
+                                    keep[i] = __float_as_uint(g / (1.0f + __expf(-g)) * u);   // (the fast division gives 0 for a denominator above 2^126)
                                 }
                             }
                             store16(p, keep, t.s0 + ck, valid, nw, lane, stg);

@@ -1,4 +1,4 @@
-"""Router logits at the ends of the range."""
+"""Router logits at the ends of the range, SwiGLU where its denominator is near the largest number."""
 import math
 
 import numpy as np
@@ -66,3 +66,20 @@ def test_route_ends_of_the_range(T, E, k, score, renorm, dtype):
     # E terms by (E/32 + 5) 2^-24, divisions by 1; weights below the normal range by their spacing
     assert np.isfinite(got).all()
     assert (np.abs(got - w) <= (2 * 32 + 16 + E / 16) * 2.0 ** -24 * np.abs(w) + 2.0 ** -126).all(), float(np.abs(got - w).max())
+
+
+# ---------------------------------------------------------------- SwiGLU
+def test_swiglu_where_the_denominator_nears_the_largest_number():
+    """silu(g) for g from -86 to -88.5 is about g e^g, 1e-36 to 1e-37; times an up projection of 2^123 it is of order 1."""
+    K, N, g = 64, 64, [-86.0, -87.0, -87.5, -88.0, -88.5, -30.0, 3.0, 0.0]
+    X = torch.zeros(len(g), K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = torch.tensor(g, device="cuda")
+    X[:, 1] = 1.0
+    W = torch.zeros(2, 1, N, K, dtype=torch.bfloat16, device="cuda")
+    W[0, :, :, 0] = 1.0
+    W[1, :, :, 1] = 2.0 ** 123
+    off = torch.tensor([0, len(g)], dtype=torch.int32, device="cuda")
+    y = uw.uw_gemm_grouped(X, W[0], off, up=W[1], out_f32=True)
+    gd, ud = X.double() @ W[0, 0].double().T, X.double() @ W[1, 0].double().T
+    zero = torch.zeros_like(gd)
+    U.check(y, U.swiglu_ref(gd, ud), U.swiglu_tolerance(gd, ud, zero, zero))
