@@ -535,6 +535,18 @@ def uw_plan_load_json(path: str, cap: int = 4096) -> list:
 # so the way to the library is kept short: one query of the current stream, no
 # context manager unless another device or stream is asked for, sizes that
 # depend on shapes alone looked up once.
+# With `stream` given, inputs have to be complete on it (as for any call that
+# takes a stream, the order is the caller's); they may be dropped right after
+# the call, and the result belongs to that stream.
+def _record(arg, stream) -> None:
+    """The memory of a tensor that `stream` is about to read or write is not given to others before it has."""
+    if isinstance(arg, torch.Tensor):
+        arg.record_stream(stream)
+    elif isinstance(arg, MxMatrix):
+        arg.codes.record_stream(stream)
+        arg.scales.record_stream(stream)
+
+
 def _run(device: torch.device, stream, fn, *args):
     """fn(stream handle, *args) with `device` current and `stream` (default:
     the device's current stream) current on it, so that allocations belong to it."""
@@ -548,6 +560,8 @@ def _run(device: torch.device, stream, fn, *args):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    for a in args:
+        _record(a, stream)
     with torch.cuda.stream(stream):
         return fn(stream.cuda_stream, *args)
 
