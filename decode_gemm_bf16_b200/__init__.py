@@ -674,6 +674,7 @@ def _mx_dequantize(handle, m, out, out_f32):
 
 
 def uw_mx_gemm_workspace(M: int, N: int, K: int, x_mx: bool = False) -> int:
+    """Workspace bytes of uw_mx_gemm on the current device."""
     n = ctypes.c_size_t()
     _check(lib().uw_mx_gemm_workspace(int(M), int(N), int(K), 1 if x_mx else 0, ctypes.byref(n)), "uw_mx_gemm_workspace")
     return n.value
@@ -719,6 +720,7 @@ class Route(NamedTuple):
 
 
 def uw_route_workspace(T: int, E: int, k: int) -> int:
+    """Workspace bytes of uw_route on the current device (0: none needed)."""
     n = ctypes.c_size_t()
     _check(lib().uw_route_workspace(int(T), int(E), int(k), ctypes.byref(n)), "uw_route_workspace")
     return n.value
@@ -784,10 +786,11 @@ def _group_bytes(a: GroupArgs) -> int:
 
 
 def uw_gemm_grouped_workspace(slots: int, W, up=None, gathered: bool = False) -> int:
-    """Workspace bytes of uw_gemm_grouped (gathered: with `rows`)."""
+    """Workspace bytes of uw_gemm_grouped (gathered: with `rows`) on the weights' device."""
     E, N, K = _expert_weight(W, "W")
-    # `rows` is read as given or not
-    return _group_bytes(_group_args(None, 0, 4 if gathered else None, int(slots), None, E, N, K, W, up, None, 0))
+    with torch.cuda.device(W.device):   # sizes follow the device's SM count
+        # `rows` is read as given or not
+        return _group_bytes(_group_args(None, 0, 4 if gathered else None, int(slots), None, E, N, K, W, up, None, 0))
 
 
 def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, up=None,

@@ -42,6 +42,23 @@ def test_a_stream_of_another_device_is_refused():
     assert not hasattr(t, "streams")
 
 
+def test_workspace_is_sized_for_the_weights_device(monkeypatch):
+    current = []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(torch.device(d))
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    seen = []
+    monkeypatch.setattr(uw, "_group_bytes", lambda a: seen.append(list(current)) or 512)
+    m = _matrix()
+    m.device = torch.device("cuda", 1)
+    assert uw.uw_gemm_grouped_workspace(6, m) == 512 and seen == [[torch.device("cuda", 1)]]
+
+
 def _calls():
     """name -> (inputs, call(inputs, stream)): every entry point that takes a stream."""
     from tests.test_gpu_experts_exact import _offsets, _rows, _weights
