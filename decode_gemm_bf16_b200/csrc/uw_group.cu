@@ -117,9 +117,8 @@ struct GroupParams {
     int64_t prep_chunk;                     // bytes of one stage of one tile there
     int part_f4;                            // float4 columns of a partial row
     uint32_t ctrl_off, stg_off, tab_off, work_off;
-    const uint8_t* sw;                      // scale tiles of W, up, X
+    const uint8_t* sw;                      // scale tiles of W, up
     const uint8_t* su;
-    const uint8_t* sx;
     int64_t w_row_tiles;                    // scale row tiles of one matrix
     int k_tiles;                            // scale tiles along k
     void* Y;
@@ -313,19 +312,10 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem16) {
     else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 
-// D (+)= A * B^T with e2m1 operands and one e8m0 scale per 32 k (K = 64).
-template <int CG>
+// D (+)= A * B^T with e2m1 operands and one e8m0 scale per 32 k (K = 64), by a pair.
 __device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t acc) {
-    if (CG == 1)
-        asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-    else
-        asm volatile(
+    asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
@@ -577,9 +567,8 @@ struct Feed {
     const uint8_t* s1;
     int sy;                      // ... their half tile (pairs)
     int half;                    // kGroupMx: a scale half tile (128 k) serves two stages
-    const uint8_t* x0;           // split rows, or the scales of 128 rows of X (and of the next 128)
-    const uint8_t* x1;
-    int xy0, xy1;                // ... their row or half tile (pairs)
+    const uint8_t* x0;           // split rows
+    int xy0, xy1;                // ... their row (pairs), or the half tile of the scales of 128 rows of X (and of the next 128)
     int bx, y, boxes, gathers;
     uint32_t x_bytes, tx;
 
@@ -599,7 +588,7 @@ struct Feed {
         tx = (uint32_t)kTileN * (SRC == kGroupMx8 ? 64u : kARow) + p.sf_b_bytes + x_bytes;
         tx += p.sf_a_bytes * (p.up && CG == 1 ? 2u : 1u);
         tx *= CG;
-        s0 = s1 = x0 = x1 = nullptr;
+        s0 = s1 = x0 = nullptr;
         sy = half = xy0 = xy1 = 0;
         if (SRC != kGroupBf16) {
             // the stage's part of a scale tile (256 k): all of it, or the half that holds the stage
@@ -622,8 +611,6 @@ struct Feed {
             // a row tile past the last reads the last one again (rows past the end: never stored)
             const int64_t rt = t.s0 / kMxTileRows, last = (p.x_rows - 1) / kMxTileRows;
             const int64_t a0 = rt * p.k_tiles + kt, a1 = (rt < last ? rt + 1 : last) * p.k_tiles + kt;
-            x0 = p.sx + a0 * kMxTileBytes;
-            x1 = p.sx + a1 * kMxTileBytes;
             xy0 = (int)(2 * a0);
             xy1 = (int)(2 * a1);
         }
@@ -666,17 +653,10 @@ struct Feed {
             return;
         }
         if (SRC == kGroupMxMx) {
-            if (CG == 1) {
-                bulk_load(st + p.off_b - p.sf_b_bytes, x0, kMxTileBytes, fb);
-                if (p.sf_b_bytes > kMxTileBytes) bulk_load(st + p.off_b - kMxTileBytes, x1, kMxTileBytes, fb);
-                x0 += kMxTileBytes;
-                x1 += kMxTileBytes;
-            } else {
-                tma_load_pair(st + p.off_b - p.sf_b_bytes, &m.sx, 0, xy0, fb);
-                if (p.sf_b_bytes > kMxTileBytes) tma_load_pair(st + p.off_b - kMxTileBytes, &m.sx, 0, xy1, fb);
-                xy0 += 2;
-                xy1 += 2;
-            }
+            tma_load_pair(st + p.off_b - p.sf_b_bytes, &m.sx, 0, xy0, fb);
+            if (p.sf_b_bytes > kMxTileBytes) tma_load_pair(st + p.off_b - kMxTileBytes, &m.sx, 0, xy1, fb);
+            xy0 += 2;
+            xy1 += 2;
         }
         if (gathers) {
 #pragma unroll
@@ -691,6 +671,7 @@ struct Feed {
 
 template <int SRC, int CG>
 __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) {
+    static_assert(SRC != kGroupMxMx || CG == 2, "4-bit rows take tiles of 128 slots at least: always pairs (pick_pair)");
     constexpr int KB = stage_k(SRC);
     constexpr bool kRe = SRC == kGroupMx;
     constexpr bool kScaled = SRC == kGroupMx8 || SRC == kGroupMxMx;   // scales in tensor memory
@@ -907,7 +888,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
                         }
 #pragma unroll
                         for (uint32_t j = 0; j < 4; j++, more = 1)
-                            tc_mma_mx<CG>(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
+                            tc_mma_mx(acc, desc(lo + 2u * j), desc(lo + lo_b + 2u * j), idesc + (j & 1u) * ((2u << 4) | (2u << 29)),
                                       sf + 4u * (j >> 1), sfx + 4u * nb * (j >> 1), more);
                     } else {
                         tc_copy_scales<CG>(sf, CG == 1 && p.up ? ss + 64u : ss);
@@ -1605,7 +1586,6 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
     p.Y = a.Y;
     p.sw = a.w_scales;
     p.su = a.up_scales;
-    p.sx = a.x_scales;
     p.w_row_tiles = mx_row_tiles(a.N);
     p.k_tiles = (int)mx_k_tiles(a.K);
     p.early = src == kGroupMx8 || h.gather;
@@ -1695,7 +1675,7 @@ cudaError_t launch_group(const GroupGemm& a, cudaStream_t s, uw_status* st) {
 
     void (*kern)(const Maps, const GroupParams) =
         src == kGroupBf16   ? (CG == 2 ? k_group<kGroupBf16, 2> : k_group<kGroupBf16, 1>)
-        : src == kGroupMxMx ? (CG == 2 ? k_group<kGroupMxMx, 2> : k_group<kGroupMxMx, 1>)
+        : src == kGroupMxMx ? k_group<kGroupMxMx, 2>
         : src == kGroupMx8  ? (CG == 2 ? k_group<kGroupMx8, 2> : k_group<kGroupMx8, 1>)
                             : k_group_rebuild;
     cudaError_t e = set_smem_attr((const void*)kern, (int)smem);
