@@ -688,7 +688,11 @@ def _mx_gemm_bytes(index: int, M: int, N: int, K: int, x_mx: bool) -> int:   # i
 def uw_mx_gemm(X, W: MxMatrix, out: Optional[torch.Tensor] = None, out_f32: bool = False, ws: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """Y[M, N] = X . W^T with W in the microscaled 4-bit form.  X: BF16 [M, K]
-    (see the header for how its values enter) or an MxMatrix (4-bit products)."""
+    or an MxMatrix (4-bit products).  BF16 values with K a multiple of 128 enter
+    as two 8-bit halves: exactly, if at least 2^-13 times the largest of their
+    block of 32 along K; below, off by at most 2^-21 (1 + 2^-8) of that largest;
+    an infinity as NaN.  With other K every value, infinities too, enters as it
+    is."""
     mx = isinstance(X, MxMatrix)
     if not mx:
         _need(X, "X", _BF16, device=W.device, contiguous=False)
@@ -798,7 +802,9 @@ def uw_gemm_grouped(X: torch.Tensor, W, offsets: torch.Tensor, rows: Optional[to
                     stream=None) -> torch.Tensor:
     """Y[s] = X[row(s)] . W[e]^T for the slots s of every expert e, that is
     offsets[e] <= s < offsets[e + 1]; with `up`, silu(X . W^T) * (X . up^T).
-    W, up: BF16 [E, N, K] or MxMatrix with a batch of E.  rows: the row of X of
+    W, up: BF16 [E, N, K] or MxMatrix with a batch of E (then values of X enter
+    as in uw_mx_gemm: with K a multiple of 128 tiny ones beside large ones are
+    rounded and infinities become NaN).  rows: the row of X of
     each slot (default: slot s reads row s).  Rows of the output outside the
     offsets are left as they were."""
     shape = _expert_weight(W, "W")
