@@ -220,6 +220,11 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// g / (1 + e^-g).  The fast division gives 0 for denominators above 2^126; a
+// quarter of either side keeps the largest finite one at 2^126.  (An exact
+// division: 128 experts of 768 x 2048 twice in 4 bits, 264 slots, 50.7 us, so 49.4.)
+__device__ __forceinline__ float silu(float g) { return __fdividef(0.25f * g, fmaf(0.25f, __expf(-g), 0.25f)); }
+
 // Y[s0 + i, nw + lane] = v[i] for 16 slots (`valid` of them in the tile), by a
 // whole warp.  A lane holds one output of 16 slots; written so, a warp's
 // store would put 2 bytes a lane into 16 rows.  Instead slots go in pairs of
@@ -1147,7 +1152,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
 #pragma unroll
                                 for (int i = i0; i < i0 + 8; i++) {
                                     const float g = __uint_as_float(first ? keep[i] : o[i]), u = __uint_as_float(first ? o[i] : keep[i]);
-                                    keep[i] = __float_as_uint(g / (1.0f + __expf(-g)) * u);   // (the fast division gives 0 for a denominator above 2^126)
+                                    keep[i] = __float_as_uint(silu(g) * u);
                                 }
                             }
                             store16(p, keep, t.s0 + ck, valid, nw, lane, stg);

@@ -71,7 +71,7 @@ def test_route_ends_of_the_range(T, E, k, score, renorm, dtype):
 # ---------------------------------------------------------------- SwiGLU
 def test_swiglu_where_the_denominator_nears_the_largest_number():
     """silu(g) for g from -86 to -88.5 is about g e^g, 1e-36 to 1e-37; times an up projection of 2^123 it is of order 1."""
-    K, N, g = 64, 64, [-86.0, -87.0, -87.5, -88.0, -88.5, -30.0, 3.0, 0.0]
+    K, N, g = 64, 64, [-86.0, -87.0, -87.5, -88.0, -88.5, -30.0, 3.0, 0.0, -0.0, 88.0, 120.0]
     X = torch.zeros(len(g), K, dtype=torch.bfloat16, device="cuda")
     X[:, 0] = torch.tensor(g, device="cuda")
     X[:, 1] = 1.0
@@ -82,4 +82,24 @@ def test_swiglu_where_the_denominator_nears_the_largest_number():
     y = uw.uw_gemm_grouped(X, W[0], off, up=W[1], out_f32=True)
     gd, ud = X.double() @ W[0, 0].double().T, X.double() @ W[1, 0].double().T
     zero = torch.zeros_like(gd)
-    U.check(y, U.swiglu_ref(gd, ud), U.swiglu_tolerance(gd, ud, zero, zero))
+    ref, tol = U.swiglu_ref(gd, ud), U.swiglu_tolerance(gd, ud, zero, zero)
+    over = ref > torch.finfo(torch.float32).max     # 88 2^123 = 2^129.5 and 120 2^123 pass the type's range
+    assert over.any(1).tolist() == [False] * 9 + [True] * 2 and y[over].isposinf().all()
+    U.check(y[~over], ref[~over], tol[~over])
+
+
+def test_swiglu_beyond_the_exponential():
+    """e^-g past the largest number: 0, as with the plain formula in fp32; infinities and NaN as it gives them."""
+    K, N, g = 64, 64, [-89.0, -1000.0, -3e38, 3e38, math.inf, -math.inf, math.nan]
+    X = torch.zeros(len(g), K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = torch.tensor(g, device="cuda")
+    X[:, 1] = 1.0
+    W = torch.zeros(2, 1, N, K, dtype=torch.bfloat16, device="cuda")
+    W[0, :, :, 0] = 1.0
+    W[1, :, :, 1] = 1.0
+    W[1, :, :, 0] = 0.0
+    off = torch.tensor([0, len(g)], dtype=torch.int32, device="cuda")
+    y = uw.uw_gemm_grouped(X[:4], W[0], torch.tensor([0, 4], dtype=torch.int32, device="cuda"), up=W[1], out_f32=True)
+    assert (y[:3] == 0).all() and torch.equal(y[3], X[3, 0].float().expand(N))
+    z = uw.uw_gemm_grouped(X, W[0], off, up=W[1], out_f32=True)
+    assert torch.equal(z[:4], y) and z[4:].isnan().all()   # (an infinity of X times the up weight 0 is NaN)
