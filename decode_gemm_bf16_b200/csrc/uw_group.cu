@@ -31,7 +31,8 @@
 //     the end: the operations of a BF16 product at twice the rate, and no
 //     rebuilt weights.  A first kernel (k_group_split) writes the rows of
 //     every tile in the order of its stages' shared memory, gathered, split
-//     and swizzled, so a stage's rows and scales are one bulk copy;
+//     and swizzled, so a stage's rows and scales are one bulk copy; for pairs
+//     with `up` it also joins the scales of the two weights;
 //   * K an odd multiple of 64 (kGroupMx): the TMA's unpacking load wants rows
 //     of 128 codes, so warps 12-19 rebuild codes to BF16 in tensor memory, the
 //     MMA's A operand;
@@ -56,12 +57,15 @@
 //     held: the power limit), tensor pipe 96 % active; one group of 8192 rows
 //     630 us, 1.53 (1.30 held, where the library's product has 1.31);
 //   4-bit weights, 128 experts of 768 x 2048 twice, 264 slots: 49 us, 3.9 TB/s
-//     of weights; 8 experts of 14336 x 4096 twice, 16 slots: 96 us, 5.2 TB/s;
-//   4-bit weights, 64 experts of 1408 x 2048 twice, 12288 slots: 149 us, 0.95
-//     PFLOP/s (22 us of it the split rows); 4480 rows of 8192 x 4096: 204 us,
-//     1.47 PFLOP/s;
-//   both in 4 bits, 2048 rows of 14336 x 4096: 51 us, 4.7 PFLOP/s; 8192^3: 192
-//     us, 5.7 PFLOP/s.
+//     of weights; 8 experts of 14336 x 4096 twice, 16 slots: 97 us, 5.1 TB/s;
+//   4-bit weights, 64 experts of 1408 x 2048 twice, 12288 slots: 151-154 us, 0.93
+//     PFLOP/s (25 us of it the split rows and joined scales); 2048 rows of 14336 x
+//     4096: 171 us, 1.41 PFLOP/s; 4096 tokens of 2 of 8 experts of that shape
+//     twice: 1346 us, 1.43 PFLOP/s (BF16 weights 1328, 1.45);
+//   K an odd multiple of 64, 14336 x 4160: one row 33 us, 0.9 TB/s of weights;
+//     2048 rows 207 us, 1.18 PFLOP/s;
+//   both in 4 bits, 2048 rows of 14336 x 4096: 52 us, 4.7 PFLOP/s, one row 12-13
+//     us; 8192^3: 192 us, 5.7 PFLOP/s.
 #include <cuda_fp16.h>
 #include <cstdlib>
 
@@ -1328,7 +1332,7 @@ __device__ __forceinline__ Split16 split16(const uint4 a, const uint4 b) {
 // 96) the first CTA takes the first 8 of W and of `up`, the second the last 8.
 // Row ((expert, 64 weight rows), k step) of `joined` is 512 bytes.  A warp joins
 // one scale tile of either weight at a time; bound by reading and writing one
-// byte per 32 weights.
+// byte per 32 weights (11.5 MB of two 64 x 1408 x 2048 weights: 3 us of the split's 25).
 __device__ __forceinline__ void join_scales(const PrepParams& p, const int32_t* count, uint32_t w0, uint32_t warps) {
     const int lane = threadIdx.x & 31;
     const uint32_t per = (uint32_t)(p.row_tiles * p.k_tiles), items = (uint32_t)p.E * per;   // (below 2^31: one CTA quantises a tile)
@@ -1354,8 +1358,8 @@ __device__ __forceinline__ void join_scales(const PrepParams& p, const int32_t* 
 // to 8, pairs 16) rows becomes row r (hi) and n + r (lo) of every stage's
 // 128-byte swizzled rows; their scale bytes lie in front as tcgen05.cp reads
 // them.  Reads and writes stay in L2 mostly (a row is read once for each of its
-// slots); bound by instructions (12288 slots of 2048: 22 us, 2.3 TB/s each way;
-// 4480 rows of 4096: 16 us).
+// slots); bound by instructions (12288 slots of 2048: 22 us, 2.3 TB/s each way,
+// 25 us with the joined scales of 64 experts of 1408 x 2048; 4480 rows of 4096: 16 us).
 __global__ void __launch_bounds__(kPrepThreads, 4) k_group_split(const PrepParams p) {
     extern __shared__ int32_t tab[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
