@@ -735,7 +735,7 @@ __device__ __forceinline__ void group_body(const Maps& m, const GroupParams& p) 
     // complete already (see k_group_split); what it writes is waited for below.
     if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     // By the warp that allocates, once it has: a dependent CTA on the same SM that took the tensor memory first would keep
-    // it while it waits for this kernel.  (By all warps after the table below: 64 rows of 14336 x 4096 17.7 us, so 16.6.)
+    // it while it waits for this kernel.  (By all warps after the table below: 64 rows of 14336 x 4096 17.7 us, so 16.7.)
     if (warp == kMma) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     list_tiles(p.offsets, p.E, p.slots, p.MG, p.n_tiles, cum, begin, count);

@@ -422,7 +422,7 @@ uw_status uw_mx_dequantize(const uw_mx_matrix* m, void* out, int out_f32, void* 
  * Y: device [M,N], BF16 or float32 (out_f32), 16-byte aligned.  M = 0 is a
  * no-op.  K above about 6 million: UW_ERR_SHAPE.  workspace: 256-byte aligned,
  * any contents, owned by the call until it completes (a captured call owns it
- * whenever its graph runs). */
+ * whenever its graph runs).  After UW_ERR_TIMEOUT: see uw_gemm_grouped. */
 uw_status uw_mx_gemm_workspace(int64_t M, int64_t N, int64_t K, int x_mx, size_t* bytes);
 
 uw_status uw_mx_gemm(const uint16_t* X, const uw_mx_matrix* X_mx, int64_t M, const uw_mx_matrix* W, void* Y, int out_f32,
